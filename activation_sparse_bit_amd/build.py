@@ -1,9 +1,9 @@
 """Compile the HIP library ``lib/libsgemv.so`` (and the measurement-only
 ``lib/libsgemv_bench.so``) in-tree for gfx950.
 
-The host packer (pack.cpp) is plain C++ built with g++; the kernels and the
-C ABI (sgemv.hip) are built with hipcc for gfx950.  All HIP code is
-compiled with packed-fp32 instructions disabled.
+The host packers (pack.cpp, pack_q4.cpp) are plain C++ built with g++; the
+kernels and the C ABI (sgemv.hip, q4.hip, norm.hip) are built with hipcc for
+gfx950.  All HIP code is compiled with packed-fp32 instructions disabled.
 """
 from __future__ import annotations
 
@@ -48,15 +48,17 @@ def build(verbose: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     obj_dir = os.path.join(LIBDIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
-    pack_o = os.path.join(obj_dir, "pack.o")
-    sgemv_o = os.path.join(obj_dir, "sgemv.o")
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-c",
-          os.path.join(CSRC, "pack.cpp"), "-o", pack_o], verbose)
-    _run([_hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, "sgemv.hip"),
-          "-o", sgemv_o], verbose)
+    objs = []
+    for name in ("pack", "pack_q4"):
+        objs.append(os.path.join(obj_dir, name + ".o"))
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-c",
+              os.path.join(CSRC, name + ".cpp"), "-o", objs[-1]], verbose)
+    for name in ("sgemv", "q4", "norm"):
+        objs.append(os.path.join(obj_dir, name + ".o"))
+        _run([_hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, name + ".hip"),
+              "-o", objs[-1]], verbose)
     tmp = LIB + ".tmp"
-    _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", sgemv_o, pack_o,
-          "-o", tmp], verbose)
+    _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     # the measurement kernels (memory ceilings), a library of their own
     bench_o = os.path.join(obj_dir, "bench_read.o")

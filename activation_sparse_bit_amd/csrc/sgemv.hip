@@ -40,7 +40,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "sgemv.h"
+#include "internal.h"
 
 extern "C" int sgemv_layout_fill_desc(int32_t N, int32_t K, int32_t tile_n, uint32_t version,
                                       sgemv_desc* d);
@@ -2040,6 +2040,11 @@ extern "C" const char* sgemv_strerror(int status) {
 }
 
 extern "C" int sgemv_last_hip_error(void) { return g_last_hip_error; }
+
+int sgemv_hip_failed(int hip_error) {
+    g_last_hip_error = hip_error;
+    return SGEMV_EHIP;
+}
 
 // ---------------------------------------------------------------------------
 // the fused call without a workspace argument

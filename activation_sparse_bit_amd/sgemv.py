@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -30,11 +31,17 @@ SGEMV_LAYOUT_NG = 3       # layout version 3: groups along N, (s, z) per column 
 SGEMV_MAX_BATCH = 16
 SGEMV_MAX_K = 65536
 SGEMV_MAX_N = 1 << 20
+SGEMV_F16, SGEMV_BF16, SGEMV_F32 = 0, 1, 2
+SGEMV_ACT_SILU, SGEMV_ACT_GELU, SGEMV_ACT_RELU = 0, 1, 2
+SGEMV_Q4_GATED, SGEMV_Q4_ZEROS, SGEMV_Q4_BF16_SCALES = 1, 2, 4
+SGEMV_NORM_POST, SGEMV_NORM_CENTER, SGEMV_NORM_PLUS_ONE = 1, 2, 4
 
 EXPORTED = ["sgemv_pack_layout", "sgemv_pack_layout_z4", "sgemv_pack_layout_ng", "sgemv_pack_layout_parts",
             "sgemv_desc_from_header",
             "sgemv_gather_indices",
             "sgemv_run", "sgemv_run_batched", "sgemv_run_fused", "sgemv_run_fused_static", "sgemv_workspace_bytes",
+            "sgemv_q4_pack", "sgemv_q4_pack_gated", "sgemv_q4_desc_from_header", "sgemv_q4_run", "sgemv_q4_run_gated",
+            "sgemv_block_norm",
             "sgemv_strerror", "sgemv_last_hip_error"]
 
 
@@ -50,6 +57,16 @@ class Desc(ctypes.Structure):
                 ("w_bytes", ctypes.c_uint64), ("m_off", ctypes.c_uint64),
                 ("m_bytes", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64),
                 ("version", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+    def as_dict(self) -> dict:
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class Q4Desc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("w_off", ctypes.c_uint64), ("w_bytes", ctypes.c_uint64),
+                ("s_off", ctypes.c_uint64), ("s_bytes", ctypes.c_uint64), ("z_off", ctypes.c_uint64),
+                ("z_bytes", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}
@@ -91,6 +108,19 @@ def lib():
     L.sgemv_run_fused_static.restype = ctypes.c_int
     L.sgemv_workspace_bytes.argtypes = [pd, i32]
     L.sgemv_workspace_bytes.restype = sz
+    pq = ctypes.POINTER(Q4Desc)
+    L.sgemv_q4_pack.argtypes = [vp, vp, vp, i32, i32, i32, u32, vp, sz, pq]
+    L.sgemv_q4_pack.restype = ctypes.c_int
+    L.sgemv_q4_pack_gated.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, u32, vp, sz, pq]
+    L.sgemv_q4_pack_gated.restype = ctypes.c_int
+    L.sgemv_q4_desc_from_header.argtypes = [vp, sz, pq]
+    L.sgemv_q4_desc_from_header.restype = ctypes.c_int
+    L.sgemv_q4_run.argtypes = [pq, vp, vp, i32, i32, i32, vp, vp, i32, i32, vp]
+    L.sgemv_q4_run.restype = ctypes.c_int
+    L.sgemv_q4_run_gated.argtypes = [pq, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, i32, vp]
+    L.sgemv_q4_run_gated.restype = ctypes.c_int
+    L.sgemv_block_norm.argtypes = [ctypes.c_char_p, vp]
+    L.sgemv_block_norm.restype = ctypes.c_int
     L.sgemv_strerror.argtypes = [ctypes.c_int]
     L.sgemv_strerror.restype = ctypes.c_char_p
     L.sgemv_last_hip_error.argtypes = []
@@ -397,6 +427,288 @@ def sgemv_run_fused_static(desc: Desc, packed, x, thresholds, y, idx=None, count
            "sgemv_run_fused_static")
 
 
+# ---------------------------------------------------------------------------
+# 4-bit products that read every weight, and the norms around a block
+# ---------------------------------------------------------------------------
+def _codes_of_torch():
+    import torch
+    return {torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32}
+
+
+_types = None      # torch dtype -> SGEMV_F16 / BF16 / F32
+_raw_stream = None
+
+
+def _type_code(t, what: str) -> int:
+    global _types
+    if _types is None:
+        _types = _codes_of_torch()
+    code = _types.get(getattr(t, "dtype", None))
+    if code is not None:
+        return code
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
+    raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected float16, bfloat16, float32")
+
+
+def _row_stride(t, what: str, M: int, n: int) -> int:
+    """Row stride of a [M][n] operand given as [n] (one row) or [M][>= n]."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 1:
+        if M != 1:
+            raise ValueError(f"{what}: one row, {M} needed")
+        if shape[0] < n:
+            raise ValueError(f"{what}: {shape[0]} elements, at least {n} needed")
+        if shape[0] > 1 and stride[0] != 1:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+        return max(shape[0], n)
+    if len(shape) != 2 or shape[0] != M or shape[1] < n:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [{M}][>= {n}]")
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if M <= 1:
+        return max(shape[1], n)
+    if stride[0] < shape[1]:
+        raise ValueError(f"{what}: rows overlap (stride {stride[0]} < {shape[1]})")
+    return stride[0]
+
+
+def _vector(t, what: str, n: int, code: int):
+    """Check an optional contiguous vector of at least n elements of a type."""
+    if t is None:
+        return None
+    if _type_code(t, what) != code:
+        raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')} differs from the operands it goes with")
+    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{n}], contiguous")
+    return t
+
+
+def _on_one_gpu(names, tensors) -> int:
+    """Index of the one GPU that holds every tensor (None is skipped)."""
+    dev = None
+    for name, t in zip(names, tensors):
+        if t is None:
+            continue
+        d = t.device
+        if d.type != "cuda":
+            raise ValueError(f"{name}: must be a GPU tensor")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name}: on {d}, the other buffers on {dev}")
+    return dev.index
+
+
+def _call_on(device: int, stream, fn, what: str):
+    """fn(stream handle) with the device current, on `stream` or on the
+    device's current stream."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+    if stream is None:
+        handle = _raw_stream(device)
+    else:
+        on = getattr(stream, "device", None)
+        if on is not None and on.index is not None and on.index != device:
+            raise ValueError(f"stream: on {on}, the buffers on cuda:{device}")
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(handle)
+    if status != SGEMV_OK:
+        raise SgemvError(status, what)
+
+
+def _host_codes(a, what: str, dtype, view=None):
+    """A contiguous NumPy array of `dtype` from a NumPy array or a torch
+    tensor (any device); 16-bit floats become their bit patterns."""
+    if not isinstance(a, np.ndarray) and hasattr(a, "detach"):
+        import torch
+        if a.dtype in (torch.float16, torch.bfloat16):
+            a = a.detach().contiguous().cpu().view(torch.int16).numpy().view(np.uint16)
+        else:
+            a = a.detach().cpu().numpy()
+    a = np.asarray(a)
+    if a.dtype == np.float16:
+        a = a.view(np.uint16) if a.flags.c_contiguous else np.ascontiguousarray(a).view(np.uint16)
+    if a.dtype != dtype:
+        raise ValueError(f"{what}: dtype {a.dtype}, expected {np.dtype(dtype).name}")
+    return np.ascontiguousarray(a)
+
+
+def _q4_part(part, group: int, what: str):
+    q, s, z = part
+    q = _host_codes(q, f"{what} codes", np.uint8)
+    s = _host_codes(s, f"{what} scales", np.uint16)
+    z = None if z is None else _host_codes(z, f"{what} zeros", np.uint8)
+    if q.ndim != 2:
+        raise ValueError(f"{what} codes: shape {q.shape}, expected [N][K]")
+    want = (q.shape[0], -(-q.shape[1] // group)) if group > 0 else None
+    for name, a in (("scales", s), ("zeros", z)):
+        if a is not None and want is not None and a.shape != want:
+            raise ValueError(f"{what} {name}: shape {a.shape}, expected {want}")
+    return q, s, z
+
+
+def _is_bf16(s) -> bool:
+    return "bfloat16" in str(getattr(s, "dtype", ""))
+
+
+def sgemv_q4_pack(q, scales, zeros=None, group: int = SGEMV_GROUP, bf16_scales: bool | None = None):
+    """Lay int4 codes q (uint8 [N][K]) with scales [N][ceil(K/group)] (float16,
+    bfloat16 or their bits as uint16) and zero-points uint8 (None: symmetric,
+    every zero-point 8) out for sgemv_q4_run.  bf16_scales says what uint16
+    scales hold (by default it follows their type).  NumPy arrays or torch
+    tensors.  Returns (Q4Desc, uint8 blob)."""
+    bf16 = _is_bf16(scales) if bf16_scales is None else bf16_scales
+    q, s, z = _q4_part((q, scales, zeros), group, "weight")
+    flags = (SGEMV_Q4_ZEROS if z is not None else 0) | (SGEMV_Q4_BF16_SCALES if bf16 else 0)
+    d = Q4Desc()
+    fn, (N, K) = lib().sgemv_q4_pack, q.shape
+    _check(fn(None, None, None, N, K, group, flags, None, 0, ctypes.byref(d)), "sgemv_q4_pack(size)")
+    blob = np.empty(d.total_bytes, dtype=np.uint8)
+    _check(fn(_ptr(q), _ptr(s), _ptr(z), N, K, group, flags, _ptr(blob), blob.nbytes, ctypes.byref(d)),
+           "sgemv_q4_pack")
+    return d, blob
+
+
+def sgemv_q4_pack_gated(gate, up, group: int = SGEMV_GROUP, bf16_scales: bool | None = None):
+    """The same for a gate and an up projection, each (q, scales, zeros) of
+    one shape and format, for sgemv_q4_run_gated."""
+    kinds = {_is_bf16(gate[1]), _is_bf16(up[1])}
+    if bf16_scales is None and len(kinds) > 1:
+        raise ValueError("gate and up scales must have one type")
+    bf16 = kinds.pop() if bf16_scales is None else bf16_scales
+    qg, sg, zg = _q4_part(gate, group, "gate")
+    qu, su, zu = _q4_part(up, group, "up")
+    if qg.shape != qu.shape or (zg is None) != (zu is None):
+        raise ValueError("gate and up must have one shape, and both zero-points or neither")
+    flags = (SGEMV_Q4_ZEROS if zg is not None else 0) | (SGEMV_Q4_BF16_SCALES if bf16 else 0)
+    d = Q4Desc()
+    fn, (N, K) = lib().sgemv_q4_pack_gated, qg.shape
+    _check(fn(None, None, None, None, None, None, N, K, group, flags, None, 0, ctypes.byref(d)),
+           "sgemv_q4_pack_gated(size)")
+    blob = np.empty(d.total_bytes, dtype=np.uint8)
+    _check(fn(_ptr(qg), _ptr(sg), _ptr(zg), _ptr(qu), _ptr(su), _ptr(zu), N, K, group, flags, _ptr(blob), blob.nbytes,
+              ctypes.byref(d)), "sgemv_q4_pack_gated")
+    return d, blob
+
+
+def sgemv_q4_desc_from_header(blob) -> Q4Desc:
+    b = np.ascontiguousarray(np.asarray(blob, dtype=np.uint8)[:256])
+    d = Q4Desc()
+    _check(lib().sgemv_q4_desc_from_header(_ptr(b), b.nbytes, ctypes.byref(d)), "sgemv_q4_desc_from_header")
+    return d
+
+
+def _q4_operands(desc, packed, x, y):
+    """Checked (x type, rows, ldx, y type, ldy) of a q4 call."""
+    xt, yt = _type_code(x, "x"), _type_code(y, "y")
+    if xt == SGEMV_F32:
+        raise ValueError("x: dtype float32, expected float16, bfloat16")
+    if yt != xt and yt != SGEMV_F32:
+        raise ValueError(f"y: dtype {str(y.dtype).replace('torch.', '')}, expected x's or float32")
+    M = 1 if x.dim() == 1 else x.shape[0]
+    _require(packed, "packed", _u8(), int(desc.total_bytes))
+    return xt, M, _row_stride(x, "x", M, desc.K), yt, _row_stride(y, "y", M, desc.N)
+
+
+def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
+    """y = W . x + bias over 4-bit weights packed by sgemv_q4_pack: x is [K]
+    or [M][>= K] with M <= 16, float16 or bfloat16; y is [N] or [M][>= N], of
+    x's type or float32; bias is [N] of x's type."""
+    xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y)
+    _vector(bias, "bias", desc.N, xt)
+    dev = _on_one_gpu(("packed", "x", "y", "bias"), (packed, x, y, bias))
+    _call_on(dev, stream, lambda s: lib().sgemv_q4_run(
+        desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, None if bias is None else bias.data_ptr(), y.data_ptr(),
+        yt, ldy, s), "sgemv_q4_run")
+
+
+_ACTS = {"silu": SGEMV_ACT_SILU, "gelu": SGEMV_ACT_GELU, "relu": SGEMV_ACT_RELU}
+
+
+def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=None, bias_up=None, stream=None):
+    """h = act(gate . x + bias_gate) * (up . x + bias_up) over 4-bit weights
+    packed by sgemv_q4_pack_gated; act is "silu", "gelu" (error function) or
+    "relu".  Operands as for sgemv_q4_run."""
+    if act not in _ACTS:
+        raise ValueError(f"act: {act!r}, expected one of {', '.join(_ACTS)}")
+    xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h)
+    _vector(bias_gate, "bias_gate", desc.N, xt)
+    _vector(bias_up, "bias_up", desc.N, xt)
+    dev = _on_one_gpu(("packed", "x", "h", "bias_gate", "bias_up"), (packed, x, h, bias_gate, bias_up))
+    _call_on(dev, stream, lambda s: lib().sgemv_q4_run_gated(
+        desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, None if bias_gate is None else bias_gate.data_ptr(),
+        None if bias_up is None else bias_up.data_ptr(), _ACTS[act], h.data_ptr(), ht, ldh, s), "sgemv_q4_run_gated")
+
+
+# struct sgemv_norm of the C header, field by field
+_NORM = struct.Struct("@qiI9P5q2f4i")
+
+
+def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bias=None, post_weight=None,
+                     post_bias=None, gate=None, scale: float = 1.0, eps: float = 1e-6, post_norm: bool | None = None,
+                     center: bool = False, plus_one: bool = False, stream=None):
+    """From a block's output y to the next block's input, in one launch:
+    r = residual + scale * gate * u with u = y, or norm(y; post_weight,
+    post_bias) when post_norm (by default: when either is given);
+    residual_out (optional) receives r, x receives norm(r; weight, bias).
+    The norm is the root mean square norm, or layer norm with center;
+    plus_one takes weights stored around zero.  x, residual, y, residual_out
+    are [D] or [rows][>= D] in float16, bfloat16 or float32 (residual_out of
+    residual's type); gate is [D] or [rows][D] of y's type; the vectors share
+    one type.  D is residual's last dimension; residual_out may be residual
+    and x may be y."""
+    rt, xt = _type_code(residual, "residual"), _type_code(x, "x")
+    rows = 1 if residual.dim() == 1 else residual.shape[0]
+    D = residual.shape[-1] if residual.dim() else 0
+    ldr, ldx = _row_stride(residual, "residual", rows, D), _row_stride(x, "x", rows, D)
+    yt, ldy, ldg, ldo, flags = rt, 0, 0, 0, 0
+    if y is not None:
+        yt, ldy = _type_code(y, "y"), _row_stride(y, "y", rows, D)
+    if residual_out is not None:
+        if _type_code(residual_out, "residual_out") != rt:
+            raise ValueError("residual_out: must have residual's type")
+        ldo = _row_stride(residual_out, "residual_out", rows, D)
+    if gate is not None:
+        if y is None or _type_code(gate, "gate") != yt:
+            raise ValueError("gate: needs y, and y's type")
+        if gate.dim() == 1:
+            _vector(gate, "gate", D, yt)
+        else:
+            ldg = _row_stride(gate, "gate", rows, D)
+    wt = None
+    for name, w in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
+        if w is not None:
+            wt = _type_code(w, name) if wt is None else wt
+            _vector(w, name, D, wt)
+    if post_norm is None:
+        post_norm = post_weight is not None or post_bias is not None
+    if post_norm:
+        flags |= SGEMV_NORM_POST
+    elif post_weight is not None or post_bias is not None:
+        raise ValueError("post_weight, post_bias: given without post_norm")
+    if post_norm and y is None:
+        raise ValueError("post_norm: needs y")
+    if center:
+        flags |= SGEMV_NORM_CENTER
+    if plus_one:
+        flags |= SGEMV_NORM_PLUS_ONE
+    tensors = (residual, y, gate, post_weight, post_bias, weight, bias, residual_out, x)
+    dev = _on_one_gpu(("residual", "y", "gate", "post_weight", "post_bias", "weight", "bias", "residual_out", "x"),
+                      tensors)
+    args = _NORM.pack(rows, D, flags, *[0 if t is None else t.data_ptr() for t in tensors], ldr, ldy, ldg, ldo, ldx,
+                      scale, eps, rt, yt, xt if wt is None else wt, xt)
+    _call_on(dev, stream, lambda s: lib().sgemv_block_norm(args, s), "sgemv_block_norm")
+
+
 def sgemv_workspace_bytes(desc: Desc, M: int = 1) -> int:
     return int(lib().sgemv_workspace_bytes(ctypes.byref(desc), M))
 
@@ -463,3 +775,20 @@ class FusedProjections:
 
     def split(self, y):
         return {name: y[..., a:a + n] for name, (a, n) in self.offsets.items()}
+
+
+class Q4Matrix:
+    """A matrix (or gate/up pair) packed for sgemv_q4_run (sgemv_q4_run_gated)
+    on the device: codes q uint8 [N][K], scales [N][ceil(K/group)], zeros
+    uint8 or None (symmetric)."""
+
+    def __init__(self, q, scales, zeros=None, group: int = SGEMV_GROUP, device="cuda", bf16_scales=None, _packed=None):
+        import torch
+        self.desc, blob = _packed or sgemv_q4_pack(q, scales, zeros, group, bf16_scales)
+        self.blob = torch.from_numpy(blob).to(device)
+        self.N, self.K = self.desc.N, self.desc.K
+
+    @classmethod
+    def gated(cls, gate, up, group: int = SGEMV_GROUP, device="cuda", bf16_scales=None):
+        """A gate and an up projection, each (q, scales, zeros)."""
+        return cls(None, None, device=device, _packed=sgemv_q4_pack_gated(gate, up, group, bf16_scales))

@@ -375,6 +375,202 @@ int sgemv_run_fused_static(const sgemv_desc* d, const void* packed, const void* 
  * description. */
 size_t sgemv_workspace_bytes(const sgemv_desc* d, int32_t M);
 
+/* ------------------------------------------------------------------------
+ * Beside the sparse projections: 4-bit products that read every weight, and
+ * the norms around a block.
+ *
+ * The calls above skip the columns that a thresholded input leaves out.  A
+ * decode step also has projections whose input is dense (an attention
+ * output, the head that gives the logits), weights quantized in other groups
+ * and widths, the gate between the up and down projections, and the norms
+ * and residual additions between the blocks.  These calls serve them with
+ * the same conventions: the caller owns every buffer, arguments are checked
+ * before any HIP call, work is enqueued on `stream` (NULL = the null stream)
+ * on the current device, which has to be the one that holds the buffers, and
+ * results are bitwise reproducible.  They need no workspace and keep no
+ * state, so calls on different streams do not disturb each other, and they
+ * may be captured into a graph.
+ * ------------------------------------------------------------------------ */
+
+enum sgemv_type {            /* element types of x, y, residuals and weights */
+    SGEMV_F16  = 0,
+    SGEMV_BF16 = 1,
+    SGEMV_F32  = 2
+};
+
+enum sgemv_act {             /* gate functions of sgemv_q4_run_gated         */
+    SGEMV_ACT_SILU = 0,      /* v / (1 + e^-v)                               */
+    SGEMV_ACT_GELU = 1,      /* v (1 + erf(v / sqrt 2)) / 2                  */
+    SGEMV_ACT_RELU = 2       /* max(v, 0)                                    */
+};
+
+#define SGEMV_Q4_GATED       1u   /* a gate and an up projection, interleaved  */
+#define SGEMV_Q4_ZEROS       2u   /* zero-points stored (else every z is 8)    */
+#define SGEMV_Q4_BF16_SCALES 4u   /* scales are bf16 instead of fp16           */
+
+/* Description of one matrix (or gate/up pair) packed by sgemv_q4_pack or
+ * sgemv_q4_pack_gated (host memory). */
+typedef struct sgemv_q4_desc {
+    int32_t  N;            /* outputs (of each of the two, when gated)     */
+    int32_t  K;            /* inputs                                       */
+    int32_t  group;        /* inputs per scale: 32, 64 or 128              */
+    uint32_t flags;        /* SGEMV_Q4_*                                   */
+    uint64_t w_off;        /* byte offset of the codes (= 256)             */
+    uint64_t w_bytes;
+    uint64_t s_off;        /* byte offset of the scales                    */
+    uint64_t s_bytes;
+    uint64_t z_off;        /* byte offset of the zero-points               */
+    uint64_t z_bytes;      /* 0 without SGEMV_Q4_ZEROS                     */
+    uint64_t total_bytes;  /* size of the whole blob                       */
+} sgemv_q4_desc;
+
+/*
+ * sgemv_q4_pack - lay 4-bit weights out for sgemv_q4_run (host only).
+ *   w^[n][k] = s[n][k/group] * (q[n][k] - z[n][k/group])
+ *
+ *   blob = header (256 B) | codes | scales | zero-points, little-endian
+ *   header 0: "SGQ1", 4: u32 version 1, 8: i32 N, 12: i32 K, 16: i32 group,
+ *          20: u32 flags, 24: u64 w_off, 32: u64 w_bytes, 40: u64 s_off,
+ *          48: u64 s_bytes, 56: u64 z_off, 64: u64 z_bytes,
+ *          72: u64 total_bytes, 80..255 zero
+ *   The matrix is cut into cells of 16 outputs by 128 inputs, zero beyond N
+ *   and K: B = ceil(K/128) cells per 16 outputs, cell (t, b) at index
+ *   t*B + b (sgemv_q4_pack_gated: the gate's cells of 16 outputs, then the
+ *   up projection's: index (2t + p)*B + b).
+ *   codes        w_off + cell*1024 + (16c + r)*16 + 4j, c, j < 4, r < 16: a
+ *                u32 whose nibble (i>>1) + 4*(i&1) is
+ *                q[16t + r][128b + 32j + 8c + i], i < 8
+ *   scales       u16 index (cell*16 + r)*P + i, P = 128/group, i < P:
+ *                s[16t + r][b*P + i], at s_off
+ *   zero-points  nibble index as for the scales, even index in the low half
+ *                of a byte, at z_off
+ *   s_off = w_off + w_bytes; z_off and total_bytes are rounded up to 256
+ *
+ *   q        host uint8 [N][K], values 0..15
+ *   scales   host uint16 [N][ceil(K/group)]: finite fp16 bits (bf16 bits with
+ *            SGEMV_Q4_BF16_SCALES)
+ *   zeros    host uint8 [N][ceil(K/group)], values 0..15, used with
+ *            SGEMV_Q4_ZEROS only; without it every zero-point is 8
+ *   N, K     1..SGEMV_MAX_N, 1..SGEMV_MAX_K, any value (the last group and
+ *            the last cells may be partial)
+ *   out      host buffer of out_capacity bytes, or NULL for a size query
+ *   desc_out receives the description (may be NULL)
+ * EINVAL for a bad group, flag, code, scale or zero-point or a NULL array;
+ * ESIZE for N, K out of range or too small a capacity.
+ */
+int sgemv_q4_pack(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros,
+                  int32_t N, int32_t K, int32_t group, uint32_t flags, void* out,
+                  size_t out_capacity, sgemv_q4_desc* desc_out);
+
+/* sgemv_q4_pack_gated - the same for a gate and an up projection of equal
+ * shape and format that share their input (SGEMV_Q4_GATED is set in the
+ * description), for sgemv_q4_run_gated. */
+int sgemv_q4_pack_gated(const uint8_t* q_gate, const uint16_t* scales_gate,
+                        const uint8_t* zeros_gate, const uint8_t* q_up,
+                        const uint16_t* scales_up, const uint8_t* zeros_up,
+                        int32_t N, int32_t K, int32_t group, uint32_t flags,
+                        void* out, size_t out_capacity, sgemv_q4_desc* desc_out);
+
+/* Parse and check the header (at least 80 bytes) of a blob of either call.
+ * EINVAL on a bad magic, version or inconsistent fields. */
+int sgemv_q4_desc_from_header(const void* header, size_t bytes,
+                              sgemv_q4_desc* desc_out);
+
+/*
+ * sgemv_q4_run - y[m][n] = sum_k w^[n][k] x[m][k] + bias[n] for 1 to
+ * SGEMV_MAX_BATCH rows, every weight read once.
+ *
+ *   d       host description without SGEMV_Q4_GATED
+ *   packed  device blob, 256-byte aligned
+ *   x       device [M][ldx] of x_type: SGEMV_F16 or SGEMV_BF16
+ *   bias    device [N] of x_type, or NULL
+ *   y       device [M][ldy] of y_type: x_type or SGEMV_F32; must not overlap
+ *           the inputs
+ *   ldx, ldy  row strides in elements, >= K and >= N.  Pointers need the
+ *           alignment of their elements only.
+ * Products are exact and sums are held in fp32, one group of inputs at a
+ * time; the group's scale, the bias and the one rounding to y_type follow.
+ * fp16 activations multiply q - z, so y is within fp32 accumulation of the
+ * exact value.  bf16 activations multiply q + 16 (four bits more than a code
+ * fit bf16's mantissa, and CDNA4 has no packed bf16 subtraction) and
+ * (z + 16) * sum x is taken off each group's sum in fp32: the accumulation
+ * error is relative to sum |s| (q + 16) |x| instead, at most a few 2^-24 of
+ * it per group, and a row with an infinity gives NaN.
+ * EINVAL for NULL, a bad type or description; ESIZE for M, ldx or ldy;
+ * EALIGN for pointers.
+ */
+int sgemv_q4_run(const sgemv_q4_desc* d, const void* packed, const void* x,
+                 int32_t x_type, int32_t M, int32_t ldx, const void* bias,
+                 void* y, int32_t y_type, int32_t ldy, void* stream);
+
+/*
+ * sgemv_q4_run_gated - the gated product of a feed-forward block in one
+ * launch:
+ *   h[m][n] = act(gate[n] . x[m] + bias_gate[n]) * (up[n] . x[m] + bias_up[n])
+ * both sums and the gate function in fp32, one rounding to h_type.  h is
+ * what the down projection takes, for instance sgemv_run_fused.
+ *
+ *   d    host description with SGEMV_Q4_GATED
+ *   act  SGEMV_ACT_*
+ *   bias_gate, bias_up  device [N] of x_type, each may be NULL
+ *   h    device [M][ldh] of h_type: x_type or SGEMV_F32
+ * Everything else as for sgemv_q4_run.
+ */
+int sgemv_q4_run_gated(const sgemv_q4_desc* d, const void* packed, const void* x,
+                       int32_t x_type, int32_t M, int32_t ldx, const void* bias_gate,
+                       const void* bias_up, int32_t act, void* h, int32_t h_type,
+                       int32_t ldh, void* stream);
+
+#define SGEMV_NORM_POST     1u   /* y is normed before it is added            */
+#define SGEMV_NORM_CENTER   2u   /* subtract the mean (layer norm)            */
+#define SGEMV_NORM_PLUS_ONE 4u   /* weights are stored around 0: factor 1 + w */
+
+/* Arguments of sgemv_block_norm (host memory, read during the call). */
+typedef struct sgemv_norm {
+    int64_t     rows;             /* 0 .. 2^31 - 1; 0 enqueues nothing (the
+                                     buffers may then be NULL)                */
+    int32_t     D;                /* 1 .. SGEMV_MAX_K                         */
+    uint32_t    flags;            /* SGEMV_NORM_*                             */
+    const void* residual;         /* device [rows][ld_residual]               */
+    const void* y;                /* device [rows][ld_y], or NULL             */
+    const void* gate;             /* device [rows][ld_gate] of y_type, or [D]
+                                     with ld_gate == 0, or NULL               */
+    const void* post_weight;      /* device [D] of w_type, each may be NULL   */
+    const void* post_bias;
+    const void* weight;
+    const void* bias;
+    void*       residual_out;     /* device [rows][ld_residual_out] of
+                                     residual_type, or NULL                   */
+    void*       x;                /* device [rows][ld_x] of x_type            */
+    int64_t     ld_residual, ld_y, ld_gate, ld_residual_out, ld_x;
+    float       scale;
+    float       eps;              /* >= 0, finite                             */
+    int32_t     residual_type, y_type, w_type, x_type;   /* SGEMV_F16/BF16/F32 */
+} sgemv_norm;
+
+/*
+ * sgemv_block_norm - from the output y of one block to the input x of the
+ * next, in one launch, one pass over the rows:
+ *   u  = y, or norm(y; post_weight, post_bias) with SGEMV_NORM_POST
+ *   r  = residual + scale * gate * u      (gate 1 when NULL)
+ *   residual_out = r
+ *   x  = norm(r; weight, bias)
+ *   norm(v; w, b) = (v - c) / sqrt(mean((v - c)^2) + eps) * w + b
+ * with c = 0, or the mean of v with SGEMV_NORM_CENTER; a NULL weight is a
+ * factor 1, a NULL bias 0, and SGEMV_NORM_PLUS_ONE adds 1 to weights that
+ * are given.  With y == NULL, r = residual (gate and SGEMV_NORM_POST are
+ * then refused).  Everything is computed in fp32 and rounded once on the way
+ * out; x is the norm of r before its rounding to residual_type.
+ *
+ * Row strides are at least D and pointers need the alignment of their
+ * elements only.  An output may be the very buffer of residual, y or a
+ * per-row gate (same address, row stride and element size); any other
+ * overlap of an output with another buffer is refused.
+ * EINVAL for NULL residual or x, a bad flag, type, eps or overlap; ESIZE for
+ * rows, D or a stride; EALIGN for pointers.
+ */
+int sgemv_block_norm(const sgemv_norm* a, void* stream);
+
 /* Static string for a status code. */
 const char* sgemv_strerror(int status);
 

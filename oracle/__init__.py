@@ -21,6 +21,8 @@ definition written out in float64:
   B[m,n]      = sum over k of |w^(n,k)| * |xe(m,k)|   (error scale)
 
 and the packed weight layout is the byte formula in ``oracle.layout``.
+``oracle.block`` holds the same kind of definitions for the 4-bit products
+that read every weight, the gated pair and the block norm.
 
 Pins: every function here is checked against values fixed independently of
 it (brute force on tiny inputs, exact rational arithmetic, closed forms and
@@ -28,8 +30,12 @@ invariants) by the CPU tests; see tests/test_oracle_*.py.
 """
 from .gemv import (GROUP, active_mask, active_indices, dequantize_columns,
                    gemv_listed, gemv_masked, gemv_dense)
+from .block import (block_norm, gate_function, norm, q4_dequantize, q4_header_fields, q4_pack_spec,
+                    q4_product, q4_scale)
 from .layout import pack_spec, unpack_spec, header_fields, read_header
 
 __all__ = ["GROUP", "active_mask", "active_indices", "dequantize_columns",
            "gemv_listed", "gemv_masked", "gemv_dense",
-           "pack_spec", "unpack_spec", "header_fields", "read_header"]
+           "pack_spec", "unpack_spec", "header_fields", "read_header",
+           "block_norm", "gate_function", "norm", "q4_dequantize", "q4_header_fields", "q4_pack_spec",
+           "q4_product", "q4_scale"]
