@@ -46,7 +46,7 @@ constexpr int kBlockK = 128;
 struct Q4Args {
     const uint8_t* w;    // codes
     const uint8_t* s;    // scales
-    const uint8_t* z;    // zero-points (NULL: 8)
+    const uint8_t* z;    // zero-points, z_stride bytes a cell
     const uint16_t* x;
     const uint16_t* bias[2];
     void* y;
@@ -56,44 +56,45 @@ struct Q4Args {
     int32_t blocks;      // blocks of 128 inputs
     int32_t gated, act;
     int32_t x_bf16, y_f32, s_bf16;
+    uint32_t z_stride, z_mask, z_set;
 };
 
 __device__ __forceinline__ float bf16_f32(uint32_t b) { return __builtin_bit_cast(float, b << 16); }
 __device__ __forceinline__ float f16_f32(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
 
-// Eight inputs of one activation row from k0 on, zero beyond K.
-__device__ __forceinline__ uint4_t load_x(const uint16_t* row, int k0, int K) {
-    uint4_t v = {0, 0, 0, 0};
-    if (k0 + 8 <= K) {
-        v = *reinterpret_cast<const uint4_u*>(row + k0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k0 + i < K) v[i >> 1] |= (uint32_t)row[k0 + i] << (16 * (i & 1));
+// Masks and exponents of the unpacking, in registers that the compiler takes
+// as unknown: with literals it emits an AND and an OR where one v_and_or_b32
+// does (a third of the unpacking).
+struct Unpack {
+    uint32_t lo, hi, exp;
+    __device__ __forceinline__ Unpack(bool bf) : lo(bf ? 0x00780078u : 0x000F000Fu), hi(0x00F000F0u),
+                                                 exp(bf ? 0x41804180u : 0x64006400u) {
+        asm("" : "+s"(lo));
+        asm("" : "+s"(hi));
+        asm("" : "+v"(exp));
     }
-    return v;
-}
+};
 
 // One word of eight codes as the fp16 integers q - z; zl is 1024 + z and zh
 // is 64 + z, twice each.
-__device__ __forceinline__ half8_t unpack_f16(uint32_t w, half2_t zl, half2_t zh) {
+__device__ __forceinline__ half8_t unpack_f16(const Unpack& u, uint32_t w, half2_t zl, half2_t zh) {
     const half2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     half2_t p[4];
-    p[0] = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u) - zl;
-    p[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u), sixteenth, -zh);
+    p[0] = __builtin_bit_cast(half2_t, (w & u.lo) | u.exp) - zl;
+    p[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & u.hi) | u.exp), sixteenth, -zh);
     w >>= 8;
-    p[2] = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u) - zl;
-    p[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u), sixteenth, -zh);
+    p[2] = __builtin_bit_cast(half2_t, (w & u.lo) | u.exp) - zl;
+    p[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & u.hi) | u.exp), sixteenth, -zh);
     return half8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
 
 // The same as the bf16 integers q + 16.
-__device__ __forceinline__ bf8_t unpack_bf16(uint32_t w) {
+__device__ __forceinline__ bf8_t unpack_bf16(const Unpack& u, uint32_t w) {
     uint4_t v;
-    v[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    v[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    v[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    v[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    v[0] = ((w << 3) & u.lo) | u.exp;
+    v[1] = ((w >> 1) & u.lo) | u.exp;
+    v[2] = ((w >> 5) & u.lo) | u.exp;
+    v[3] = ((w >> 9) & u.lo) | u.exp;
     return __builtin_bit_cast(bf8_t, v);
 }
 
@@ -103,21 +104,56 @@ __device__ __forceinline__ float gate_of(float v, int act) {
     return v < 0.0f ? 0.0f : v;   // a NaN stays
 }
 
+// The scales of a lane's output in one block of 128 inputs (P of them) and
+// their zero-points, as loaded: whole words, of which a lane takes its part
+// when it uses them.  (Loads of 8 or 16 bits are widened by the compiler where
+// they meet the loop, which waits for them there and leaves nothing in flight.)
+template <int P>
+struct Meta {
+    typedef uint32_t words __attribute__((ext_vector_type(P == 4 ? 2 : 1)));
+    words s;
+    uint32_t z;
+    // Without zero-points every lane rereads one line of the scales (stride 0): no branch, so that the number of
+    // loads in flight is known where they are waited for.
+    __device__ __forceinline__ void load(const Q4Args& a, int64_t cell, int n16) {
+        s = reinterpret_cast<const words*>(a.s + cell * 32 * P)[P == 1 ? n16 >> 1 : n16];
+        z = reinterpret_cast<const uint32_t*>(a.z + cell * a.z_stride)[n16 * P >> 3];
+    }
+    __device__ __forceinline__ float scale(int g, int n16, bool bf16) const {
+        const uint32_t word = P == 4 ? s[g >> 1] : s[0];
+        const uint32_t b = word >> (P == 1 ? (n16 & 1) * 16 : (g & 1) * 16);
+        const float f = f16_f32(b & 0xFFFFu), h = bf16_f32(b);
+        return bf16 ? h : f;
+    }
+    __device__ __forceinline__ uint32_t zero(const Q4Args& a, int g, int n16) const {
+        return ((z >> ((n16 * P & 7) * 4 + g * 4)) & a.z_mask) | a.z_set;   // masks 15 and 0, or 0 and 8
+    }
+};
+
 // BF: bf16 activations.  NT: tiles per workgroup (even when gated: a gate
-// tile, then its up tile).  MR: result registers in use, ceil(M / 4).
-// P: groups per block of 128 inputs.
+// tile, then its up tile).  MR: result registers in use: 1, 2, 4 for up to
+// 4, 8, 16 rows.  P: groups per block of 128 inputs.
 template <bool BF, int NT, int MR, int P>
 __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
-    extern __shared__ float red[];   // [wavefront][NT][MR][64]
+    constexpr int J = 4 / MR;   // steps that share an operand of activations
+    extern __shared__ uint4_t lds[];   // MR * 64 for each wavefront: activations, then its sums [NT][MR][64]
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int n16 = lane & 15;
     const int c = lane >> 4;
-    const int row = (n16 >> 2) + (n16 & 3) * 4;   // the activation row this lane feeds
     const int tile0 = blockIdx.x * NT;
-    const uint16_t* xrow = a.x + (int64_t)row * a.ldx;
-    const bool feeds = row < a.M;
+    // Load l of a block's activations: row 4 l + c, its inputs from 8 * n16 on (the last row again beyond M: those
+    // results are not stored).
+    const uint16_t* xlane[MR];
+    uint4_t *put[MR], *get[MR];   // where this lane writes what it loads, and reads what it feeds
+#pragma unroll
+    for (int l = 0; l < MR; ++l) {
+        const int r = 4 * l + c, j = n16 >> 2;
+        xlane[l] = a.x + (int64_t)min(r, a.M - 1) * a.ldx + 8 * n16;
+        put[l] = lds + wave * MR * 64 + r * 16 + ((J * (r + (n16 & 3) + 4 * (j / J)) + j % J) & 15);
+        get[l] = lds + wave * MR * 64 + n16 / J * 16 + ((n16 + J * (c + 4 * l)) & 15);
+    }
 
     int cell[NT];   // first cell of each tile (a tile past the end rereads the last one)
 #pragma unroll
@@ -129,62 +165,128 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
 #pragma unroll
         for (int i = 0; i < MR; ++i) sum[t][i] = 0.0f;
 
-    for (int b = wave; b < a.blocks; b += waves) {
-        uint4_t x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = uint4_t{0, 0, 0, 0};
-            if (feeds) x[j] = load_x(xrow, b * kBlockK + 32 * j + 8 * c, a.K);
-        }
+    const auto fetch_weights = [&](uint4_t (&w)[NT], Meta<P> (&md)[NT], int b) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int64_t cl = cell[t] + b;
-            const uint4_t w = reinterpret_cast<const uint4_t*>(a.w + cl * 1024)[lane];
-            const int64_t sx = (cl * kTileN + n16) * P;   // scale index of this lane's first group
+            w[t] = reinterpret_cast<const uint4_t*>(a.w + (int64_t)(cell[t] + b) * 1024)[lane];
+            md[t].load(a, cell[t] + b, n16);
+        }
+    };
+    const Unpack u(BF);
+    const auto multiply = [&](const uint4_t (&w)[NT], const Meta<P> (&md)[NT], const uint4_t (&raw)[MR]) {
+        // From rows to operands through the wavefront's own LDS (its accesses are in order; the fences hold the
+        // compiler to it).
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int g = 0; g < P; ++g) {
-                const uint32_t sb = reinterpret_cast<const uint16_t*>(a.s)[sx + g];
-                const float s = a.s_bf16 ? bf16_f32(sb) : f16_f32(sb);
-                uint32_t z = 8;
-                if (a.z) z = (a.z[(sx + g) >> 1] >> (((sx + g) & 1) * 4)) & 15u;
-                float4_t acc = {0, 0, 0, 0};
-                if constexpr (BF) {
-                    float4_t ones = {0, 0, 0, 0};
-                    const uint4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        for (int l = 0; l < MR; ++l) *put[l] = raw[l];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        uint4_t x[MR];
 #pragma unroll
-                    for (int j = g * 4 / P; j < (g + 1) * 4 / P; ++j) {
-                        const bf8_t xv = __builtin_bit_cast(bf8_t, x[j]);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, unpack_bf16(w[j]), acc, 0, 0, 0);
-                        ones = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, __builtin_bit_cast(bf8_t, one), ones, 0, 0, 0);
-                    }
-                    const float off = -(float)(16u + z);
+        for (int h = 0; h < MR; ++h) x[h] = *get[h];
 #pragma unroll
-                    for (int i = 0; i < MR; ++i) sum[t][i] = fmaf(s, fmaf(off, ones[i], acc[i]), sum[t][i]);
-                } else {
-                    const half2_t zl = __builtin_bit_cast(half2_t, (0x6400u | z) * 0x10001u);   // 1024 + z
-                    const half2_t zh = zl - half2_t{(_Float16)960.0f, (_Float16)960.0f};        // 64 + z
+        for (int g = 0; g < P; ++g) {
+            constexpr int kSteps = 4 / P;                    // steps of a group
+            constexpr int kPhases = kSteps < J ? kSteps : J;   // ... of different operand rows
+            float ones[MR];   // BF: the group's sum of activations
+            if constexpr (BF) {
+                const uint4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+                float4_t o = {0, 0, 0, 0};
 #pragma unroll
-                    for (int j = g * 4 / P; j < (g + 1) * 4 / P; ++j)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, x[j]),
-                                                                     unpack_f16(w[j], zl, zh), acc, 0, 0, 0);
+                for (int h = g * kSteps / J; h <= ((g + 1) * kSteps - 1) / J; ++h)
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, x[h]),
+                                                                __builtin_bit_cast(bf8_t, one), o, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < MR; ++i) sum[t][i] = fmaf(s, acc[i], sum[t][i]);
+                for (int i = 0; i < MR; ++i) {
+                    ones[i] = o[i * J + g * kSteps % J];
+#pragma unroll
+                    for (int q = 1; q < kPhases; ++q) ones[i] += o[i * J + (g * kSteps + q) % J];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float s = md[t].scale(g, n16, a.s_bf16);
+                const uint32_t z = md[t].zero(a, g, n16);
+                const half2_t zl = __builtin_bit_cast(half2_t, (0x6400u | z) * 0x10001u);   // 1024 + z
+                const half2_t zh = zl - half2_t{(_Float16)960.0f, (_Float16)960.0f};        // 64 + z
+                float4_t acc[kPhases];
+#pragma unroll
+                for (int q = 0; q < kPhases; ++q) acc[q] = float4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) {
+                    const int j = g * kSteps + e;
+                    float4_t& d = acc[e % kPhases];
+                    if constexpr (BF)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, x[j / J]),
+                                                                    unpack_bf16(u, w[t][j]), d, 0, 0, 0);
+                    else
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, x[j / J]),
+                                                                   unpack_f16(u, w[t][j], zl, zh), d, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < MR; ++i) {
+                    float v = acc[0][i * J + g * kSteps % J];
+#pragma unroll
+                    for (int q = 1; q < kPhases; ++q) v += acc[q][i * J + (g * kSteps + q) % J];
+                    if constexpr (BF) v = fmaf(-(float)(16u + z), ones[i], v);
+                    sum[t][i] = fmaf(s, v, sum[t][i]);
                 }
             }
         }
+        // Consume the products here: moved behind a branch, the first read of a result can come too soon after the
+        // matrix instruction (seen with this compiler: the last block's product was lost).
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MR; ++i) asm volatile("" : "+v"(sum[t][i]));
+    };
+
+    const int full = a.K / kBlockK;
+    uint4_t w[NT], raw[MR];
+    Meta<P> md[NT];
+    if (full < a.blocks && wave == full % waves) {   // the inputs behind the last full block
+        fetch_weights(w, md, full);
+        const int k0 = full * kBlockK + 8 * n16;
+#pragma unroll
+        for (int l = 0; l < MR; ++l) {
+            const uint16_t* row = xlane[l] - 8 * n16;
+            uint32_t e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = row[min(k0 + i, a.K - 1)];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = k0 + i < a.K ? e[i] : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[l][i] = e[2 * i] | e[2 * i + 1] << 16;
+        }
+        multiply(w, md, raw);
+    }
+    // wavefront w multiplies blocks w, w + waves, ...: the workgroup reads
+    // one contiguous run at a time
+    for (int b = wave; b < full; b += waves) {
+        fetch_weights(w, md, b);
+#pragma unroll
+        for (int l = 0; l < MR; ++l) raw[l] = *reinterpret_cast<const uint4_u*>(xlane[l] + b * kBlockK);
+        multiply(w, md, raw);
     }
 
+    // a wavefront's sums take the place of its activations
+    float* red = reinterpret_cast<float*>(lds);
+    constexpr int kStride = MR * 256;   // floats of a wavefront's LDS
+    static_assert(NT * MR * 64 <= kStride, "sums fit");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < MR; ++i) red[((wave * NT + t) * MR + i) * 64 + lane] = sum[t][i];
+        for (int i = 0; i < MR; ++i) red[wave * kStride + (t * MR + i) * 64 + lane] = sum[t][i];
     __syncthreads();
 
     const int per_wave = NT * MR * 64;
     const int outs = a.gated ? per_wave / 2 : per_wave;
     for (int o = threadIdx.x; o < outs; o += blockDim.x) {
         const int l = o & 63, i = (o >> 6) % MR, t = (o >> 6) / MR;
-        const int m = (l >> 4) + 4 * i;
+        const int m = (l >> 4) * MR + i;
         const int tile = a.gated ? (tile0 >> 1) + t : tile0 + t;   // tile of the output
         const int n = tile * kTileN + (l & 15);
         if (m >= a.M || n >= a.N) continue;
@@ -194,7 +296,7 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
             v[p] = 0.0f;
             if (p && !a.gated) break;
             const float* src = red + (((a.gated ? 2 * t + p : t) * MR + i) * 64 + l);
-            for (int w = 0; w < waves; ++w) v[p] += src[w * per_wave];
+            for (int w = 0; w < waves; ++w) v[p] += src[w * kStride];
             if (a.bias[p]) v[p] += BF ? bf16_f32(a.bias[p][n]) : f16_f32(a.bias[p][n]);
         }
         const float r = a.gated ? gate_of(v[0], a.act) * v[1] : v[0];
@@ -215,6 +317,21 @@ Kernel pick_p(int P) {
 template <bool BF, int NT>
 Kernel pick_mr(int MR, int P) {
     return MR == 1 ? pick_p<BF, NT, 1>(P) : MR == 2 ? pick_p<BF, NT, 2>(P) : pick_p<BF, NT, 4>(P);
+}
+
+template <bool BF>
+Kernel pick(int NT, int MR, int P) {
+    return NT == 1 ? pick_mr<BF, 1>(MR, P) : NT == 2 ? pick_mr<BF, 2>(MR, P) : pick_p<BF, 4, 4>(P);
+}
+
+int launch(const Q4Args& a, Kernel k, int NT, int waves, hipStream_t stream) {
+    const int MR = a.M <= 4 ? 1 : a.M <= 8 ? 2 : 4;
+    const size_t lds = (size_t)waves * MR * 1024;
+    Q4Args copy = a;
+    void* args[] = {&copy};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((a.tiles + NT - 1) / NT),
+                                         dim3(waves * 64), args, lds, stream);
+    return e == hipSuccess ? SGEMV_OK : sgemv_hip_failed((int)e);
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -238,7 +355,11 @@ int run(const sgemv_q4_desc* d, const void* packed, const void* x, int x_type, i
     std::memset(&a, 0, sizeof a);
     a.w = blob + d->w_off;
     a.s = blob + d->s_off;
-    a.z = (d->flags & SGEMV_Q4_ZEROS) ? blob + d->z_off : nullptr;
+    const bool zeros = (d->flags & SGEMV_Q4_ZEROS) != 0;
+    a.z = zeros ? blob + d->z_off : a.s;
+    a.z_stride = zeros ? kTileN / 2 * (kBlockK / d->group) : 0;
+    a.z_mask = zeros ? 15 : 0;
+    a.z_set = zeros ? 0 : 8;
     a.x = static_cast<const uint16_t*>(x);
     a.bias[0] = static_cast<const uint16_t*>(bias0);
     a.bias[1] = static_cast<const uint16_t*>(bias1);
@@ -256,19 +377,25 @@ int run(const sgemv_q4_desc* d, const void* packed, const void* x, int x_type, i
     a.y_f32 = y_type == SGEMV_F32;
     a.s_bf16 = (d->flags & SGEMV_Q4_BF16_SCALES) != 0;
 
-    const int NT = gated ? 2 : 1;
     const int MR = M <= 4 ? 1 : M <= 8 ? 2 : 4;
-    const int P = kBlockK / d->group;
-    int waves = 4;
+    // Tiles per workgroup.  More tiles share one reading of the activations, fewer leave no compute unit idle: below
+    // 512 tiles one each (4096 x 14336: 7.3 us against 10.2 with two), from there two (8192 x 28672, eight rows: 26.7
+    // against 31.9 with one), and with more than eight rows, whose activations weigh most, four from 1024 tiles on
+    // (28672 x 8192, 16 rows: 29.4 against 34.5 with two).
+    int NT = a.tiles < 512 ? 1 : MR == 4 && a.tiles >= 1024 ? 4 : 2;
+    if (gated && NT == 1) NT = 2;
+    // Wavefronts, which split the inputs: sixteen where the workgroups alone do not fill the card (4096 x 14336: 7.3 us
+    // against 9.4 with eight; 28672 x 8192, one row, 896 workgroups: 23.8 against 25.3), eight otherwise
+    // (14336 x 4096, 16 rows, gated: 13.8 against 15.3 with sixteen), four for many short rows
+    // (100003 x 1024: 10.7 against 11.5 with eight).
+    const int grid = (a.tiles + NT - 1) / NT;
+    int waves = 8;
+    if (MR == 4 ? grid <= 256 && a.blocks >= 32 : (grid <= 512 && a.blocks >= 32) || (grid <= 1024 && a.blocks >= 64))
+        waves = 16;
+    else if (a.blocks <= 8 && grid > 1024) waves = 4;
     while (waves > 1 && waves > a.blocks) waves /= 2;
-    Kernel k;
-    if (a.x_bf16) k = NT == 1 ? pick_mr<true, 1>(MR, P) : pick_mr<true, 2>(MR, P);
-    else k = NT == 1 ? pick_mr<false, 1>(MR, P) : pick_mr<false, 2>(MR, P);
-    const size_t lds = (size_t)waves * NT * MR * 64 * sizeof(float);
-    void* args[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((a.tiles + NT - 1) / NT),
-                                         dim3(waves * 64), args, lds, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? SGEMV_OK : sgemv_hip_failed((int)e);
+    const int P = kBlockK / d->group;
+    return launch(a, a.x_bf16 ? pick<true>(NT, MR, P) : pick<false>(NT, MR, P), NT, waves, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace

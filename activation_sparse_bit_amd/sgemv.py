@@ -430,24 +430,28 @@ def sgemv_run_fused_static(desc: Desc, packed, x, thresholds, y, idx=None, count
 # ---------------------------------------------------------------------------
 # 4-bit products that read every weight, and the norms around a block
 # ---------------------------------------------------------------------------
-def _codes_of_torch():
+_TYPES: dict = {}     # torch dtype -> SGEMV_F16 / BF16 / F32, filled on the first call
+_torch = None
+_raw_stream = None    # device index -> handle of its current stream
+_device_now = None    # -> index of the current device
+
+
+def _load_torch():
+    global _torch, _raw_stream, _device_now
     import torch
-    return {torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32}
-
-
-_types = None      # torch dtype -> SGEMV_F16 / BF16 / F32
-_raw_stream = None
+    _TYPES.update({torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _torch = torch
 
 
 def _type_code(t, what: str) -> int:
-    global _types
-    if _types is None:
-        _types = _codes_of_torch()
-    code = _types.get(getattr(t, "dtype", None))
+    if _torch is None:
+        _load_torch()
+    code = _TYPES.get(getattr(t, "dtype", None))
     if code is not None:
         return code
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected float16, bfloat16, float32")
 
@@ -455,6 +459,14 @@ def _type_code(t, what: str) -> int:
 def _row_stride(t, what: str, M: int, n: int) -> int:
     """Row stride of a [M][n] operand given as [n] (one row) or [M][>= n]."""
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and shape[0] == M and shape[1] >= n:
+        if shape[1] > 1 and stride[1] != 1:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+        if M <= 1:
+            return max(shape[1], n)
+        if stride[0] < shape[1]:
+            raise ValueError(f"{what}: rows overlap (stride {stride[0]} < {shape[1]})")
+        return stride[0]
     if len(shape) == 1:
         if M != 1:
             raise ValueError(f"{what}: one row, {M} needed")
@@ -463,64 +475,53 @@ def _row_stride(t, what: str, M: int, n: int) -> int:
         if shape[0] > 1 and stride[0] != 1:
             raise ValueError(f"{what}: the last dimension must be contiguous")
         return max(shape[0], n)
-    if len(shape) != 2 or shape[0] != M or shape[1] < n:
-        raise ValueError(f"{what}: shape {tuple(shape)}, expected [{M}][>= {n}]")
-    if shape[1] > 1 and stride[1] != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    if M <= 1:
-        return max(shape[1], n)
-    if stride[0] < shape[1]:
-        raise ValueError(f"{what}: rows overlap (stride {stride[0]} < {shape[1]})")
-    return stride[0]
+    raise ValueError(f"{what}: shape {tuple(shape)}, expected [{M}][>= {n}]")
 
 
-def _vector(t, what: str, n: int, code: int):
-    """Check an optional contiguous vector of at least n elements of a type."""
+def _vector(t, what: str, n: int, code: int) -> int:
+    """Address of an optional contiguous vector of at least n elements."""
     if t is None:
-        return None
+        return 0
     if _type_code(t, what) != code:
         raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')} differs from the operands it goes with")
     if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{n}], contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _on_one_gpu(names, tensors) -> int:
-    """Index of the one GPU that holds every tensor (None is skipped)."""
-    dev = None
-    for name, t in zip(names, tensors):
-        if t is None:
-            continue
-        d = t.device
-        if d.type != "cuda":
-            raise ValueError(f"{name}: must be a GPU tensor")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{name}: on {d}, the other buffers on {dev}")
-    return dev.index
-
-
-def _call_on(device: int, stream, fn, what: str):
-    """fn(stream handle) with the device current, on `stream` or on the
-    device's current stream."""
-    global _raw_stream
-    import torch
-    if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda i: torch.cuda.current_stream(i).cuda_stream)
+def _stream_on(device, stream):
+    """Handle of `stream`, or of the current stream of `device`."""
     if stream is None:
-        handle = _raw_stream(device)
+        return _raw_stream(device.index)
+    on = getattr(stream, "device", None)
+    if on is not None and on.index is not None and on.index != device.index:
+        raise ValueError(f"stream: on {on}, the buffers on {device}")
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on_one_gpu(device, **tensors):
+    """Every tensor (None is skipped) lives on `device`, a GPU."""
+    if device.type == "cuda":
+        for t in tensors.values():
+            if t is not None and t.device != device:
+                break
+        else:
+            return
+    for what, t in tensors.items():
+        if t is not None and t.device.type != "cuda":
+            raise ValueError(f"{what}: must be a GPU tensor")
+    for what, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{what}: on {t.device}, other buffers on {device}")
+
+
+def _call(fn, device, args, what: str):
+    """fn(*args) with `device` current; a bad status becomes SgemvError."""
+    if _device_now() == device.index:
+        status = fn(*args)
     else:
-        on = getattr(stream, "device", None)
-        if on is not None and on.index is not None and on.index != device:
-            raise ValueError(f"stream: on {on}, the buffers on cuda:{device}")
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == device:
-        status = fn(handle)
-    else:
-        with torch.cuda.device(device):
-            status = fn(handle)
+        with _torch.cuda.device(device):
+            status = fn(*args)
     if status != SGEMV_OK:
         raise SgemvError(status, what)
 
@@ -614,21 +615,26 @@ def _q4_operands(desc, packed, x, y):
         raise ValueError("x: dtype float32, expected float16, bfloat16")
     if yt != xt and yt != SGEMV_F32:
         raise ValueError(f"y: dtype {str(y.dtype).replace('torch.', '')}, expected x's or float32")
+    if not (type(packed) is _torch.Tensor and packed.dtype is _torch.uint8 and packed.is_contiguous()
+            and packed.numel() >= desc.total_bytes):
+        if isinstance(packed, int):
+            raise ValueError("packed: expected a torch tensor, got int")
+        _require(packed, "packed", _u8(), int(desc.total_bytes))
     M = 1 if x.dim() == 1 else x.shape[0]
-    _require(packed, "packed", _u8(), int(desc.total_bytes))
     return xt, M, _row_stride(x, "x", M, desc.K), yt, _row_stride(y, "y", M, desc.N)
 
 
 def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
     """y = W . x + bias over 4-bit weights packed by sgemv_q4_pack: x is [K]
     or [M][>= K] with M <= 16, float16 or bfloat16; y is [N] or [M][>= N], of
-    x's type or float32; bias is [N] of x's type."""
+    x's type or float32; bias is [N] of x's type.  Runs on `stream`, or on the
+    current stream of the tensors' device."""
     xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y)
-    _vector(bias, "bias", desc.N, xt)
-    dev = _on_one_gpu(("packed", "x", "y", "bias"), (packed, x, y, bias))
-    _call_on(dev, stream, lambda s: lib().sgemv_q4_run(
-        desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, None if bias is None else bias.data_ptr(), y.data_ptr(),
-        yt, ldy, s), "sgemv_q4_run")
+    b = _vector(bias, "bias", desc.N, xt)
+    device = x.device
+    _on_one_gpu(device, packed=packed, x=x, y=y, bias=bias)
+    _call(lib().sgemv_q4_run, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, b, y.data_ptr(), yt, ldy,
+                                       _stream_on(device, stream)), "sgemv_q4_run")
 
 
 _ACTS = {"silu": SGEMV_ACT_SILU, "gelu": SGEMV_ACT_GELU, "relu": SGEMV_ACT_RELU}
@@ -641,12 +647,11 @@ def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=
     if act not in _ACTS:
         raise ValueError(f"act: {act!r}, expected one of {', '.join(_ACTS)}")
     xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h)
-    _vector(bias_gate, "bias_gate", desc.N, xt)
-    _vector(bias_up, "bias_up", desc.N, xt)
-    dev = _on_one_gpu(("packed", "x", "h", "bias_gate", "bias_up"), (packed, x, h, bias_gate, bias_up))
-    _call_on(dev, stream, lambda s: lib().sgemv_q4_run_gated(
-        desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, None if bias_gate is None else bias_gate.data_ptr(),
-        None if bias_up is None else bias_up.data_ptr(), _ACTS[act], h.data_ptr(), ht, ldh, s), "sgemv_q4_run_gated")
+    bg, bu = _vector(bias_gate, "bias_gate", desc.N, xt), _vector(bias_up, "bias_up", desc.N, xt)
+    device = x.device
+    _on_one_gpu(device, packed=packed, x=x, h=h, bias_gate=bias_gate, bias_up=bias_up)
+    _call(lib().sgemv_q4_run_gated, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, bg, bu, _ACTS[act],
+                                             h.data_ptr(), ht, ldh, _stream_on(device, stream)), "sgemv_q4_run_gated")
 
 
 # struct sgemv_norm of the C header, field by field
@@ -670,43 +675,46 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
     rows = 1 if residual.dim() == 1 else residual.shape[0]
     D = residual.shape[-1] if residual.dim() else 0
     ldr, ldx = _row_stride(residual, "residual", rows, D), _row_stride(x, "x", rows, D)
-    yt, ldy, ldg, ldo, flags = rt, 0, 0, 0, 0
+    device, flags = residual.device, 0
+    yt, ldy, yp, ldg, gp, ldo, op = rt, 0, 0, 0, 0, 0, 0
     if y is not None:
-        yt, ldy = _type_code(y, "y"), _row_stride(y, "y", rows, D)
+        yt, ldy, yp = _type_code(y, "y"), _row_stride(y, "y", rows, D), y.data_ptr()
     if residual_out is not None:
         if _type_code(residual_out, "residual_out") != rt:
             raise ValueError("residual_out: must have residual's type")
-        ldo = _row_stride(residual_out, "residual_out", rows, D)
+        ldo, op = _row_stride(residual_out, "residual_out", rows, D), residual_out.data_ptr()
     if gate is not None:
         if y is None or _type_code(gate, "gate") != yt:
             raise ValueError("gate: needs y, and y's type")
         if gate.dim() == 1:
-            _vector(gate, "gate", D, yt)
+            gp = _vector(gate, "gate", D, yt)
         else:
-            ldg = _row_stride(gate, "gate", rows, D)
-    wt = None
-    for name, w in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
+            ldg, gp = _row_stride(gate, "gate", rows, D), gate.data_ptr()
+    wt, wp = xt, [0, 0, 0, 0]
+    vectors = (post_weight, post_bias, weight, bias)
+    for i, w in enumerate(vectors):
         if w is not None:
-            wt = _type_code(w, name) if wt is None else wt
-            _vector(w, name, D, wt)
+            name = ("post_weight", "post_bias", "weight", "bias")[i]
+            if not any(wp):
+                wt = _type_code(w, name)
+            wp[i] = _vector(w, name, D, wt)
     if post_norm is None:
         post_norm = post_weight is not None or post_bias is not None
     if post_norm:
         flags |= SGEMV_NORM_POST
+        if y is None:
+            raise ValueError("post_norm: needs y")
     elif post_weight is not None or post_bias is not None:
         raise ValueError("post_weight, post_bias: given without post_norm")
-    if post_norm and y is None:
-        raise ValueError("post_norm: needs y")
     if center:
         flags |= SGEMV_NORM_CENTER
     if plus_one:
         flags |= SGEMV_NORM_PLUS_ONE
-    tensors = (residual, y, gate, post_weight, post_bias, weight, bias, residual_out, x)
-    dev = _on_one_gpu(("residual", "y", "gate", "post_weight", "post_bias", "weight", "bias", "residual_out", "x"),
-                      tensors)
-    args = _NORM.pack(rows, D, flags, *[0 if t is None else t.data_ptr() for t in tensors], ldr, ldy, ldg, ldo, ldx,
-                      scale, eps, rt, yt, xt if wt is None else wt, xt)
-    _call_on(dev, stream, lambda s: lib().sgemv_block_norm(args, s), "sgemv_block_norm")
+    _on_one_gpu(device, residual=residual, x=x, y=y, residual_out=residual_out, gate=gate, post_weight=post_weight,
+                post_bias=post_bias, weight=weight, bias=bias)
+    args = _NORM.pack(rows, D, flags, residual.data_ptr(), yp, gp, *wp, op, x.data_ptr(), ldr, ldy, ldg, ldo, ldx,
+                      scale, eps, rt, yt, wt, xt)
+    _call(lib().sgemv_block_norm, device, (args, _stream_on(device, stream)), "sgemv_block_norm")
 
 
 def sgemv_workspace_bytes(desc: Desc, M: int = 1) -> int:
