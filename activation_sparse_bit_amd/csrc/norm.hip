@@ -9,6 +9,12 @@
 // deviations are two sums over the row each (the deviations are taken from
 // the mean, not from a difference of large sums), added over the lanes of a
 // wavefront and then over the wavefronts in a fixed order.
+//
+// A thread owns runs of eight elements, moved as 16-byte pieces at whatever
+// address the row has (pieces off a 16-byte boundary cost 3 to 7 % here), and
+// the first threads own one element each of what a width that is no multiple
+// of eight leaves over.  No element has two owners, so outputs may take the
+// place of inputs.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -23,70 +29,88 @@ typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t uint4_u2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t uint4_u4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight elements as loaded: 16 bytes of 16-bit types, 32 bytes of fp32.
-template <int BYTES>
+// N elements (a run of eight, or one) as loaded: words of BYTES-wide elements.
+template <int BYTES, int N>
 struct Raw {
-    uint4_t v[BYTES / 2];
+    uint4_t v[N == 8 ? BYTES / 2 : 1];
+
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        if constexpr (N == 1) {
+            if constexpr (BYTES == 2) v[0][0] = static_cast<const uint16_t*>(p)[at];
+            else v[0][0] = static_cast<const uint32_t*>(p)[at];
+        } else if constexpr (BYTES == 2) {
+            v[0] = *reinterpret_cast<const uint4_u2*>(static_cast<const uint16_t*>(p) + at);
+        } else {
+            const uint32_t* q = static_cast<const uint32_t*>(p) + at;
+            v[0] = *reinterpret_cast<const uint4_u4*>(q);
+            v[1] = *reinterpret_cast<const uint4_u4*>(q + 4);
+        }
+    }
+
+    __device__ __forceinline__ void get(int type, float (&f)[N]) const {
+        // words by value: a bit cast of a vector element itself reads element 0
+        if constexpr (BYTES == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t e = v[i >> 2][i & 3];
+                f[i] = __builtin_bit_cast(float, e);
+            }
+        } else if (type == SGEMV_BF16) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t e = v[0][i >> 1];
+                f[i] = __builtin_bit_cast(float, (i & 1) ? e & 0xFFFF0000u : e << 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t e = v[0][i >> 1];
+                f[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(e >> (16 * (i & 1))));
+            }
+        }
+    }
 };
 
-// Elements e0 .. e0 + 8 of a row, zero beyond D.
-template <int BYTES>
-__device__ __forceinline__ Raw<BYTES> load8(const void* p, int64_t row, int e0, int D) {
-    Raw<BYTES> r;
+// The same for a vector (weights, biases) whose type is known at run time
+// only; absent where p is NULL.
+template <int N>
+struct RawAny {
+    uint4_t v[N == 8 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void* p, int type, int64_t at) {
+        if (!p) return;
+        if (type == SGEMV_F32) {
+            Raw<4, N> r;
+            r.load(p, at);
 #pragma unroll
-    for (int i = 0; i < BYTES / 2; ++i) r.v[i] = uint4_t{0, 0, 0, 0};
-    if constexpr (BYTES == 2) {
-        const uint16_t* q = static_cast<const uint16_t*>(p) + row + e0;
-        if (e0 + 8 <= D) {
-            r.v[0] = *reinterpret_cast<const uint4_u2*>(q);
+            for (int i = 0; i < (N == 8 ? 2 : 1); ++i) v[i] = r.v[i];
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e0 + i < D) r.v[0][i >> 1] |= (uint32_t)q[i] << (16 * (i & 1));
-        }
-    } else {
-        const uint32_t* q = static_cast<const uint32_t*>(p) + row + e0;
-        if (e0 + 8 <= D) {
-            r.v[0] = *reinterpret_cast<const uint4_u4*>(q);
-            r.v[1] = *reinterpret_cast<const uint4_u4*>(q + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e0 + i < D) r.v[i >> 2][i & 3] = q[i];
+            Raw<2, N> r;
+            r.load(p, at);
+            v[0] = r.v[0];
         }
     }
-    return r;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void to_f32(const Raw<BYTES>& r, bool bf16, float* f) {
-    if constexpr (BYTES == 4) {
+    __device__ __forceinline__ void get(int type, float (&f)[N]) const {
+        if (type == SGEMV_F32) {
+            Raw<4, N> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t e = r.v[i >> 2][i & 3];   // by value: a bit cast of the vector element itself reads element 0
-            f[i] = __builtin_bit_cast(float, e);
+            for (int i = 0; i < (N == 8 ? 2 : 1); ++i) r.v[i] = v[i];
+            r.get(type, f);
+        } else {
+            Raw<2, N> r;
+            r.v[0] = v[0];
+            r.get(type, f);
         }
-    } else if (bf16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = __builtin_bit_cast(float, (i & 1) ? r.v[0][i >> 1] & 0xFFFF0000u : r.v[0][i >> 1] << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.v[0][i >> 1] >> (16 * (i & 1))));
     }
-}
+};
 
-// A vector of length D (weights, a shared gate) in any type.
-__device__ __forceinline__ void load8_any(const void* p, int type, int64_t row, int e0, int D, float* f) {
-    if (type == SGEMV_F32) to_f32<4>(load8<4>(p, row, e0, D), false, f);
-    else to_f32<2>(load8<2>(p, row, e0, D), type == SGEMV_BF16, f);
-}
-
-__device__ __forceinline__ void store8(void* p, int type, int64_t row, int e0, int D, const float* f) {
+template <int N>
+__device__ __forceinline__ void store(void* p, int type, int64_t at, const float (&f)[N]) {
     if (type == SGEMV_F32) {
-        float* q = static_cast<float*>(p) + row + e0;
-        if (e0 + 8 <= D) {
+        float* q = static_cast<float*>(p) + at;
+        if constexpr (N == 1) {
+            q[0] = f[0];
+        } else {
             uint4_t a, b;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -95,165 +119,272 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t row, int e0, i
             }
             *reinterpret_cast<uint4_u4*>(q) = a;
             *reinterpret_cast<uint4_u4*>(q + 4) = b;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e0 + i < D) q[i] = f[i];
         }
         return;
     }
-    uint16_t h[8];
+    uint16_t h[N];
     if (type == SGEMV_BF16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)f[i]);
+        for (int i = 0; i < N; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)f[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = __builtin_bit_cast(uint16_t, (_Float16)f[i]);
+        for (int i = 0; i < N; ++i) h[i] = __builtin_bit_cast(uint16_t, (_Float16)f[i]);
     }
-    uint16_t* q = static_cast<uint16_t*>(p) + row + e0;
-    if (e0 + 8 <= D) {
+    uint16_t* q = static_cast<uint16_t*>(p) + at;
+    if constexpr (N == 1) {
+        q[0] = h[0];
+    } else {
         uint4_t a;
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
         *reinterpret_cast<uint4_u2*>(q) = a;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (e0 + i < D) q[i] = h[i];
     }
 }
 
-// Sum of v over the T threads of a row, the same value in each.  `slot`
-// names the call: two calls in a row use two places, so one barrier each.
-template <int T>
+// Sum of v over a row's threads, the same value in each.  `slot` names the
+// call: calls that follow each other use different places, so one barrier
+// each.
+template <bool WAVE>
 __device__ __forceinline__ float row_sum(float v, float (*part)[16], int slot) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    if constexpr (T > 64) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) part[slot][wave] = v;
+    if constexpr (!WAVE) {
+        const int waves = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < T / 64; ++w) v += part[slot][w];
+        v = part[slot][0];
+        for (int w = 1; w < waves; ++w) v += part[slot][w];
     }
     return v;
 }
 
-// v <- (v - c) / sqrt(mean((v - c)^2) + eps) over the row; elements beyond D
-// (zero on entry) do not count.
-template <int T, int CH>
-__device__ __forceinline__ void normalize(float (&v)[CH * 8], int tid, const sgemv_norm& a, float (*part)[16],
-                                          int slot) {
+// Everything a thread holds of a row and where it is: CH runs, and with ODD
+// one element more.
+template <int CH, bool ODD>
+struct Mine {
+    int run0, step;       // element of the first run, distance of the runs
+    int full, D;          // D rounded down to a multiple of eight
+    int odd_at;           // the odd element
+    bool has_odd;
+
+    __device__ __forceinline__ int at(int c) const { return run0 + c * step; }
+    __device__ __forceinline__ bool in(int c) const { return at(c) < full; }
+    // where to load from: threads behind the last run read it again
+    __device__ __forceinline__ int from(int c) const { return min(at(c), full - 8); }
+    __device__ __forceinline__ int odd_from() const { return min(odd_at, D - 1); }
+};
+
+template <int CH>
+struct Values {
+    float v[CH][8];
+    float odd[1];
+
+    // zero what is not the row's (most wavefronts have nothing of the kind)
+    template <bool ODD>
+    __device__ __forceinline__ void clear_outside(const Mine<CH, ODD>& my) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (!my.in(c)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
+            }
+        if (ODD && !my.has_odd) odd[0] = 0.0f;
+    }
+};
+
+// v <- (v - c) / sqrt(mean((v - c)^2) + eps) over the row.  What lies outside
+// the row has to be zero on entry, and does not count.
+template <bool WAVE, int CH, bool ODD>
+__device__ __forceinline__ void normalize(Values<CH>& x, const Mine<CH, ODD>& my, const sgemv_norm& a,
+                                          float (*part)[16], int slot) {
     const float inv_d = 1.0f / (float)a.D;
     if (a.flags & SGEMV_NORM_CENTER) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CH * 8; ++i) s += v[i];
-        const float mean = row_sum<T>(s, part, slot) * inv_d;
+        float s = ODD ? x.odd[0] : 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((c * T + tid) * 8 + i < a.D) v[c * 8 + i] -= mean;
-    }
-    float q = 0.0f;
+            for (int i = 0; i < 8; ++i) s += x.v[c][i];
+        const float mean = row_sum<WAVE>(s, part, slot) * inv_d;
 #pragma unroll
-    for (int i = 0; i < CH * 8; ++i) q = fmaf(v[i], v[i], q);
-    const float inv = 1.0f / sqrtf(row_sum<T>(q, part, slot + 1) * inv_d + a.eps);
+        for (int c = 0; c < CH; ++c) {
+            const float m = my.in(c) ? mean : 0.0f;
 #pragma unroll
-    for (int i = 0; i < CH * 8; ++i) v[i] *= inv;
-}
-
-// v <- v * w + b for the eight elements from e0 on.
-__device__ __forceinline__ void affine(float* v, const void* w, const void* b, const sgemv_norm& a, int e0) {
-    float t[8];
-    if (w) {
-        load8_any(w, a.w_type, 0, e0, a.D, t);
-        const float one = (a.flags & SGEMV_NORM_PLUS_ONE) ? 1.0f : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= t[i] + one;
-    }
-    if (b) {
-        load8_any(b, a.w_type, 0, e0, a.D, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += t[i];
-    }
-}
-
-// T threads a row, CH chunks of eight elements a thread (D <= 8 * T * CH).
-// RB, YB: bytes of an element of the residual and of y.
-template <int T, int CH, int RB, int YB>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm(sgemv_norm a) {
-    __shared__ float part[4][16];
-    constexpr int kRows = T < 256 ? 256 / T : 1;   // rows per workgroup
-    const int tid = threadIdx.x % T;
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
-    if (row >= a.rows) return;   // only where a wavefront owns a row: no barrier follows there
-    const int D = a.D;
-
-    Raw<RB> rr[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) rr[c] = load8<RB>(a.residual, row * a.ld_residual, (c * T + tid) * 8, D);
-    float r[CH * 8];
-    if (a.y) {
-        Raw<YB> yr[CH];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) yr[c] = load8<YB>(a.y, row * a.ld_y, (c * T + tid) * 8, D);
-        float u[CH * 8];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) to_f32<YB>(yr[c], a.y_type == SGEMV_BF16, u + c * 8);
-        if (a.flags & SGEMV_NORM_POST) {
-            normalize<T, CH>(u, tid, a, part, 0);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) affine(u + c * 8, a.post_weight, a.post_bias, a, (c * T + tid) * 8);
+            for (int i = 0; i < 8; ++i) x.v[c][i] -= m;
         }
-        if (a.gate) {
+        if (ODD && my.has_odd) x.odd[0] -= mean;
+    }
+    float q = ODD ? x.odd[0] * x.odd[0] : 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = fmaf(x.v[c][i], x.v[c][i], q);
+    const float inv = 1.0f / sqrtf(row_sum<WAVE>(q, part, slot + 1) * inv_d + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.v[c][i] *= inv;
+    if (ODD) x.odd[0] *= inv;
+}
+
+// A weight and a bias of N elements.
+template <int N>
+struct Affine {
+    RawAny<N> w, b;
+    __device__ __forceinline__ void load(const void* pw, const void* pb, int type, int64_t at) {
+        w.load(pw, type, at);
+        b.load(pb, type, at);
+    }
+    __device__ __forceinline__ void apply(float (&v)[N], const void* pw, const void* pb, const sgemv_norm& a) const {
+        float t[N];
+        if (pw) {
+            w.get(a.w_type, t);
+            const float one = (a.flags & SGEMV_NORM_PLUS_ONE) ? 1.0f : 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] *= t[i] + one;
+        }
+        if (pb) {
+            b.get(a.w_type, t);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += t[i];
+        }
+    }
+};
+
+// A row's threads (a wavefront with WAVE, four rows a workgroup; a workgroup
+// otherwise) own CH runs each.  RB, YB: bytes of an element of the residual
+// and of y.  ODD: D is no multiple of eight.  A thread with one run loads all
+// that it will need at once, so that a lone row waits for memory once; one
+// with many loads what it has registers for.
+template <bool WAVE, int CH, int RB, int YB, bool ODD>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
+    __shared__ float part[4][16];
+    constexpr bool kAll = CH == 1, kBoth = CH <= 2;   // every vector, or the residual beside y, loaded up front
+    const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+    if (WAVE && row >= a.rows) return;   // no barrier follows with WAVE
+    Mine<CH, ODD> my;
+    my.run0 = tid * 8;
+    my.step = (WAVE ? 64 : blockDim.x) * 8;
+    my.D = a.D;
+    my.full = a.D & ~7;
+    my.odd_at = my.full + tid;
+    my.has_odd = ODD && my.odd_at < a.D;
+    const int64_t rrow = row * a.ld_residual, yrow = row * a.ld_y, grow = row * a.ld_gate;
+    const int64_t orow = row * a.ld_residual_out, xrow = row * a.ld_x;
+
+    Raw<RB, 8> rr[CH];
+    Raw<YB, 8> yr[CH], gr[CH];
+    Affine<8> post, pre;
+    Raw<RB, 1> rr1;
+    Raw<YB, 1> yr1, gr1;
+    Affine<1> post1, pre1;
+    if (!ODD || my.full) {   // a row of fewer than eight has no run
+        if (a.y) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) yr[c].load(a.y, yrow + my.from(c));
+        }
+        if (kBoth || !a.y) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) rr[c].load(a.residual, rrow + my.from(c));
+        }
+        if (kBoth && a.gate) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) gr[c].load(a.gate, grow + my.from(c));
+        }
+        if (kAll) {
+            post.load(a.post_weight, a.post_bias, a.w_type, my.from(0));
+            pre.load(a.weight, a.bias, a.w_type, my.from(0));
+        }
+    }
+    if (ODD) {
+        if (a.y) yr1.load(a.y, yrow + my.odd_from());
+        rr1.load(a.residual, rrow + my.odd_from());
+        if (a.gate) gr1.load(a.gate, grow + my.odd_from());
+        post1.load(a.post_weight, a.post_bias, a.w_type, my.odd_from());
+        pre1.load(a.weight, a.bias, a.w_type, my.odd_from());
+    }
+
+    Values<CH> r;
+    if (a.y) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) yr[c].get(a.y_type, r.v[c]);
+        if (ODD) yr1.get(a.y_type, r.odd);
+        if (a.flags & SGEMV_NORM_POST) {
+            r.clear_outside(my);
+            normalize<WAVE, CH, ODD>(r, my, a, part, 0);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                float g[8];
-                load8_any(a.gate, a.y_type, row * a.ld_gate, (c * T + tid) * 8, D, g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[c * 8 + i] *= g[i];
+                if (!kBoth) asm volatile("" ::: "memory");   // one run's loads at a time: the registers are full
+                if (!kAll) post.load(a.post_weight, a.post_bias, a.w_type, my.from(c));
+                post.apply(r.v[c], a.post_weight, a.post_bias, a);
             }
+            if (ODD) post1.apply(r.odd, a.post_weight, a.post_bias, a);
         }
 #pragma unroll
-        for (int c = 0; c < CH; ++c) to_f32<RB>(rr[c], a.residual_type == SGEMV_BF16, r + c * 8);
+        for (int c = 0; c < CH; ++c) {
+            if (!kBoth) {
+                asm volatile("" ::: "memory");
+                rr[c].load(a.residual, rrow + my.from(c));
+                if (a.gate) gr[c].load(a.gate, grow + my.from(c));
+            }
+            float t[8];
+            if (a.gate) {
+                gr[c].get(a.y_type, t);
 #pragma unroll
-        for (int i = 0; i < CH * 8; ++i) r[i] = fmaf(a.scale, u[i], r[i]);
+                for (int i = 0; i < 8; ++i) r.v[c][i] *= t[i];
+            }
+            rr[c].get(a.residual_type, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.v[c][i] = fmaf(a.scale, r.v[c][i], t[i]);
+        }
+        if (ODD) {
+            float t[1];
+            if (a.gate) {
+                gr1.get(a.y_type, t);
+                r.odd[0] *= t[0];
+            }
+            rr1.get(a.residual_type, t);
+            r.odd[0] = fmaf(a.scale, r.odd[0], t[0]);
+        }
     } else {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) to_f32<RB>(rr[c], a.residual_type == SGEMV_BF16, r + c * 8);
+        for (int c = 0; c < CH; ++c) rr[c].get(a.residual_type, r.v[c]);
+        if (ODD) rr1.get(a.residual_type, r.odd);
     }
     if (a.residual_out) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-            if ((c * T + tid) * 8 < D)
-                store8(a.residual_out, a.residual_type, row * a.ld_residual_out, (c * T + tid) * 8, D, r + c * 8);
+            if (my.in(c)) store(a.residual_out, a.residual_type, orow + my.at(c), r.v[c]);
+        if (ODD && my.has_odd) store(a.residual_out, a.residual_type, orow + my.odd_at, r.odd);
     }
-    // elements beyond D are not zero here where a shift or scale moved them
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if ((c * T + tid) * 8 + i >= D) r[c * 8 + i] = 0.0f;
-    normalize<T, CH>(r, tid, a, part, 2);
+    r.clear_outside(my);
+    normalize<WAVE, CH, ODD>(r, my, a, part, 2);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int e0 = (c * T + tid) * 8;
-        if (e0 < D) {
-            affine(r + c * 8, a.weight, a.bias, a, e0);
-            store8(a.x, a.x_type, row * a.ld_x, e0, D, r + c * 8);
+        if (my.in(c)) {
+            if (!kBoth) asm volatile("" ::: "memory");
+            if (!kAll) pre.load(a.weight, a.bias, a.w_type, my.at(c));
+            pre.apply(r.v[c], a.weight, a.bias, a);
+            store(a.x, a.x_type, xrow + my.at(c), r.v[c]);
         }
+    }
+    if (ODD && my.has_odd) {
+        pre1.apply(r.odd, a.weight, a.bias, a);
+        store(a.x, a.x_type, xrow + my.odd_at, r.odd);
     }
 }
 
 typedef void (*Kernel)(sgemv_norm);
 
-template <int T, int CH>
+template <bool WAVE, int CH, bool ODD>
 Kernel pick_types(int RB, int YB) {
-    if (RB == 2) return YB == 2 ? k_norm<T, CH, 2, 2> : k_norm<T, CH, 2, 4>;
-    return YB == 2 ? k_norm<T, CH, 4, 2> : k_norm<T, CH, 4, 4>;
+    if (RB == 2) return YB == 2 ? k_norm<WAVE, CH, 2, 2, ODD> : k_norm<WAVE, CH, 2, 4, ODD>;
+    return YB == 2 ? k_norm<WAVE, CH, 4, 2, ODD> : k_norm<WAVE, CH, 4, 4, ODD>;
+}
+
+template <bool WAVE, int CH>
+Kernel pick(int RB, int YB, bool odd) {
+    return odd ? pick_types<WAVE, CH, true>(RB, YB) : pick_types<WAVE, CH, false>(RB, YB);
 }
 
 int size_of(int type) { return type == SGEMV_F32 ? 4 : 2; }
@@ -324,17 +455,30 @@ extern "C" int sgemv_block_norm(const sgemv_norm* args, void* stream) {
         for (const Rows& b : others)
             if (clash(o, b, a.D)) return SGEMV_EINVAL;
 
+    const bool odd = a.D % 8 != 0;
+    const int runs = a.D / 8;
     Kernel k;
-    int T, rows_per = 1;
-    if (a.D <= 512) { T = 64; k = pick_types<64, 1>(rb, yb); rows_per = 4; }
-    else if (a.D <= 2048) { T = 256; k = pick_types<256, 1>(rb, yb); }
-    else if (a.D <= 4096) { T = 256; k = pick_types<256, 2>(rb, yb); }
-    else if (a.D <= 8192) { T = 256; k = pick_types<256, 4>(rb, yb); }
-    else if (a.D <= 16384) { T = 512; k = pick_types<512, 4>(rb, yb); }
-    else if (a.D <= 32768) { T = 1024; k = pick_types<1024, 4>(rb, yb); }
-    else { T = 1024; k = pick_types<1024, 8>(rb, yb); }
+    unsigned block = 256, rows_per = 1;
+    if (runs <= 64) {
+        k = pick<true, 1>(rb, yb, odd);
+        rows_per = 4;
+    } else {
+        // Runs a thread.  One is fastest for a few rows, where only latency counts (16 x 4096: 4.4 us, 5.4 with two);
+        // many rows want several runs in flight a thread and room for more rows on a compute unit (8192 x 4096: 53 us
+        // with two runs, 67 with one, 65 with four; 2048 x 14336: 65 us with four, 70 with two).
+        int CH = 1;
+        if (runs > 512 || (runs > 128 && a.rows > 512)) CH = 2;
+        if (runs > 2048 || (runs > 1024 && a.rows > 256)) CH = 4;
+        if (runs > 4096) CH = 8;
+        block = (unsigned)((runs + CH * 64 - 1) / (CH * 64) * 64);
+        k = CH == 1   ? pick<false, 1>(rb, yb, odd)
+            : CH == 2 ? pick<false, 2>(rb, yb, odd)
+            : CH == 4 ? pick<false, 4>(rb, yb, odd)
+                      : pick<false, 8>(rb, yb, odd);
+    }
     void* kargs[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((unsigned)((a.rows + rows_per - 1) / rows_per)),
-                                         dim3(T < 256 ? 256 : T), kargs, 0, static_cast<hipStream_t>(stream));
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k),
+                                         dim3((unsigned)((a.rows + rows_per - 1) / rows_per)), dim3(block), kargs, 0,
+                                         static_cast<hipStream_t>(stream));
     return e == hipSuccess ? SGEMV_OK : sgemv_hip_failed((int)e);
 }

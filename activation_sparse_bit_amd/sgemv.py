@@ -446,11 +446,12 @@ def _load_torch():
 
 
 def _type_code(t, what: str) -> int:
-    if _torch is None:
-        _load_torch()
-    code = _TYPES.get(getattr(t, "dtype", None))
-    if code is not None:
-        return code
+    try:
+        return _TYPES[t.dtype]
+    except (KeyError, AttributeError):
+        if _torch is None:
+            _load_torch()
+            return _type_code(t, what)
     if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected float16, bfloat16, float32")
@@ -499,18 +500,18 @@ def _stream_on(device, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _on_one_gpu(device, **tensors):
+def _on_one_gpu(device, names, tensors):
     """Every tensor (None is skipped) lives on `device`, a GPU."""
     if device.type == "cuda":
-        for t in tensors.values():
+        for t in tensors:
             if t is not None and t.device != device:
                 break
         else:
             return
-    for what, t in tensors.items():
+    for what, t in zip(names, tensors):
         if t is not None and t.device.type != "cuda":
             raise ValueError(f"{what}: must be a GPU tensor")
-    for what, t in tensors.items():
+    for what, t in zip(names, tensors):
         if t is not None and t.device != device:
             raise ValueError(f"{what}: on {t.device}, other buffers on {device}")
 
@@ -632,7 +633,7 @@ def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
     xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y)
     b = _vector(bias, "bias", desc.N, xt)
     device = x.device
-    _on_one_gpu(device, packed=packed, x=x, y=y, bias=bias)
+    _on_one_gpu(device, ("packed", "x", "y", "bias"), (packed, x, y, bias))
     _call(lib().sgemv_q4_run, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, b, y.data_ptr(), yt, ldy,
                                        _stream_on(device, stream)), "sgemv_q4_run")
 
@@ -649,7 +650,7 @@ def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=
     xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h)
     bg, bu = _vector(bias_gate, "bias_gate", desc.N, xt), _vector(bias_up, "bias_up", desc.N, xt)
     device = x.device
-    _on_one_gpu(device, packed=packed, x=x, h=h, bias_gate=bias_gate, bias_up=bias_up)
+    _on_one_gpu(device, ("packed", "x", "h", "bias_gate", "bias_up"), (packed, x, h, bias_gate, bias_up))
     _call(lib().sgemv_q4_run_gated, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, bg, bu, _ACTS[act],
                                              h.data_ptr(), ht, ldh, _stream_on(device, stream)), "sgemv_q4_run_gated")
 
@@ -690,14 +691,19 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
             gp = _vector(gate, "gate", D, yt)
         else:
             ldg, gp = _row_stride(gate, "gate", rows, D), gate.data_ptr()
-    wt, wp = xt, [0, 0, 0, 0]
-    vectors = (post_weight, post_bias, weight, bias)
-    for i, w in enumerate(vectors):
-        if w is not None:
-            name = ("post_weight", "post_bias", "weight", "bias")[i]
-            if not any(wp):
-                wt = _type_code(w, name)
-            wp[i] = _vector(w, name, D, wt)
+    wt, w0, w1, w2, w3 = -1, 0, 0, 0, 0
+    if weight is not None:
+        wt = _type_code(weight, "weight")
+        w2 = _vector(weight, "weight", D, wt)
+    if bias is not None:
+        wt = _type_code(bias, "bias") if wt < 0 else wt
+        w3 = _vector(bias, "bias", D, wt)
+    if post_weight is not None:
+        wt = _type_code(post_weight, "post_weight") if wt < 0 else wt
+        w0 = _vector(post_weight, "post_weight", D, wt)
+    if post_bias is not None:
+        wt = _type_code(post_bias, "post_bias") if wt < 0 else wt
+        w1 = _vector(post_bias, "post_bias", D, wt)
     if post_norm is None:
         post_norm = post_weight is not None or post_bias is not None
     if post_norm:
@@ -710,10 +716,10 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
         flags |= SGEMV_NORM_CENTER
     if plus_one:
         flags |= SGEMV_NORM_PLUS_ONE
-    _on_one_gpu(device, residual=residual, x=x, y=y, residual_out=residual_out, gate=gate, post_weight=post_weight,
-                post_bias=post_bias, weight=weight, bias=bias)
-    args = _NORM.pack(rows, D, flags, residual.data_ptr(), yp, gp, *wp, op, x.data_ptr(), ldr, ldy, ldg, ldo, ldx,
-                      scale, eps, rt, yt, wt, xt)
+    _on_one_gpu(device, ("residual", "x", "y", "residual_out", "gate", "weight", "bias", "post_weight", "post_bias"),
+                (residual, x, y, residual_out, gate, weight, bias, post_weight, post_bias))
+    args = _NORM.pack(rows, D, flags, residual.data_ptr(), yp, gp, w0, w1, w2, w3, op, x.data_ptr(), ldr, ldy, ldg,
+                      ldo, ldx, scale, eps, rt, yt, wt if wt >= 0 else xt, xt)
     _call(lib().sgemv_block_norm, device, (args, _stream_on(device, stream)), "sgemv_block_norm")
 
 
