@@ -310,6 +310,79 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// packing on the device
+// ---------------------------------------------------------------------------
+struct PackArgs {
+    const uint8_t* q[2];
+    const uint16_t* s[2];
+    const uint8_t* z[2];
+    uint8_t* blob;
+    sgemv_q4_desc d;
+};
+
+// A thread writes 16 bytes: the codes of one lane in one cell, the header,
+// or scales and zero-points.  Bound by reading a byte a code; rows are read
+// in pieces of eight bytes, which the caches put together.
+__global__ __launch_bounds__(256) void k_q4_pack(PackArgs a) {
+    const uint64_t blocks = (a.d.K + kBlockK - 1) / kBlockK, parts = (a.d.flags & SGEMV_Q4_GATED) ? 2 : 1;
+    const uint64_t slots = a.d.w_bytes / 16, P = kBlockK / a.d.group;
+    const uint64_t N = a.d.N, K = a.d.K, G = (K + a.d.group - 1) / a.d.group;
+    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id < slots) {
+        const uint64_t cell = id >> 6, r = id & 15, c = id >> 4 & 3;
+        const uint64_t b = cell % blocks, tile = cell / blocks, n = tile / parts * kTileN + r;
+        const uint8_t* row = a.q[tile % parts] + n * K;
+        uint4_t out = {0, 0, 0, 0};
+        if (n < N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t k0 = b * kBlockK + 32 * j + 8 * c;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (k0 + i < K) out[j] |= (uint32_t)(row[k0 + i] & 15) << (4 * ((i >> 1) + 4 * (i & 1)));
+            }
+        }
+        reinterpret_cast<uint4_t*>(a.blob + a.d.w_off)[id] = out;
+        return;
+    }
+    // the bytes outside the codes, 16 at a time: the header, then scales and zero-points up to the end
+    const uint64_t rest = id - slots;
+    const uint64_t at = rest < 16 ? rest * 16 : a.d.s_off + (rest - 16) * 16;
+    if (at >= a.d.total_bytes) return;
+    uint8_t byte[16];
+    for (int i = 0; i < 16; ++i) {
+        const uint64_t o = at + i;
+        uint32_t v = 0;
+        const auto index = [&](uint64_t m, uint64_t& n, uint64_t& g, uint64_t& part) {
+            const uint64_t cell = m / (kTileN * P), tile = cell / blocks;
+            n = tile / parts * kTileN + m / P % kTileN;
+            g = cell % blocks * P + m % P;
+            part = tile % parts;
+            return n < N && g < G;
+        };
+        uint64_t n, g, part;
+        if (o < 80) {
+            const uint32_t word[20] = {0x31514753u, 1u, (uint32_t)a.d.N, (uint32_t)a.d.K, (uint32_t)a.d.group, a.d.flags,
+                                       (uint32_t)a.d.w_off, (uint32_t)(a.d.w_off >> 32), (uint32_t)a.d.w_bytes,
+                                       (uint32_t)(a.d.w_bytes >> 32), (uint32_t)a.d.s_off, (uint32_t)(a.d.s_off >> 32),
+                                       (uint32_t)a.d.s_bytes, (uint32_t)(a.d.s_bytes >> 32), (uint32_t)a.d.z_off,
+                                       (uint32_t)(a.d.z_off >> 32), (uint32_t)a.d.z_bytes, (uint32_t)(a.d.z_bytes >> 32),
+                                       (uint32_t)a.d.total_bytes, (uint32_t)(a.d.total_bytes >> 32)};
+            v = word[o >> 2] >> (8 * (o & 3));
+        } else if (o >= a.d.s_off && o < a.d.s_off + a.d.s_bytes) {
+            const uint64_t m = (o - a.d.s_off) >> 1;
+            if (index(m, n, g, part)) v = a.s[part][n * G + g] >> (8 * (o & 1));
+        } else if (o >= a.d.z_off && o < a.d.z_off + a.d.z_bytes) {
+            const uint64_t m = (o - a.d.z_off) << 1;
+            if (index(m, n, g, part)) v = a.z[part][n * G + g] & 15;
+            if (index(m + 1, n, g, part)) v |= (uint32_t)(a.z[part][n * G + g] & 15) << 4;
+        }
+        byte[i] = (uint8_t)v;
+    }
+    for (int i = 0; i < 16; ++i) a.blob[at + i] = byte[i];
+}
+
 typedef void (*Kernel)(Q4Args);
 
 template <bool BF, int NT, int MR, bool ST>
@@ -420,4 +493,36 @@ extern "C" int sgemv_q4_run_gated(const sgemv_q4_desc* d, const void* packed, co
                                   int32_t M, int32_t ldx, const void* bias_gate, const void* bias_up, int32_t act,
                                   void* h, int32_t h_type, int32_t ldh, void* stream) {
     return run(d, packed, x, x_type, M, ldx, bias_gate, bias_up, act, h, h_type, ldh, true, stream);
+}
+
+extern "C" int sgemv_q4_pack_device(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros, const uint8_t* q_up,
+                                    const uint16_t* scales_up, const uint8_t* zeros_up, int32_t N, int32_t K,
+                                    int32_t group, uint32_t flags, void* packed, size_t capacity,
+                                    sgemv_q4_desc* desc_out, void* stream) {
+    PackArgs a;
+    std::memset(&a, 0, sizeof a);
+    const bool gated = (flags & SGEMV_Q4_GATED) != 0, with_zeros = (flags & SGEMV_Q4_ZEROS) != 0;
+    const int st = gated ? sgemv_q4_pack_gated(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, N, K, group, flags,
+                                               nullptr, 0, &a.d)
+                         : sgemv_q4_pack(nullptr, nullptr, nullptr, N, K, group, flags, nullptr, 0, &a.d);
+    if (st) return st;
+    if (!q || !scales || (with_zeros && !zeros)) return SGEMV_EINVAL;
+    if (gated && (!q_up || !scales_up || (with_zeros && !zeros_up))) return SGEMV_EINVAL;
+    if (!packed) return SGEMV_EINVAL;
+    if (capacity < a.d.total_bytes) return SGEMV_ESIZE;
+    if (!aligned_to(packed, 256) || !aligned_to(scales, 2) || !aligned_to(scales_up, 2)) return SGEMV_EALIGN;
+    a.q[0] = q;
+    a.q[1] = q_up;
+    a.s[0] = scales;
+    a.s[1] = scales_up;
+    a.z[0] = zeros;
+    a.z[1] = zeros_up;
+    a.blob = static_cast<uint8_t*>(packed);
+    const uint64_t threads = a.d.w_bytes / 16 + 16 + (a.d.total_bytes - a.d.s_off + 15) / 16;
+    void* args[] = {&a};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k_q4_pack), dim3((unsigned)((threads + 255) / 256)),
+                                         dim3(256), args, 0, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return sgemv_hip_failed((int)e);
+    if (desc_out) *desc_out = a.d;
+    return SGEMV_OK;
 }

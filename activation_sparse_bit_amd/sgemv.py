@@ -40,7 +40,8 @@ EXPORTED = ["sgemv_pack_layout", "sgemv_pack_layout_z4", "sgemv_pack_layout_ng",
             "sgemv_desc_from_header",
             "sgemv_gather_indices",
             "sgemv_run", "sgemv_run_batched", "sgemv_run_fused", "sgemv_run_fused_static", "sgemv_workspace_bytes",
-            "sgemv_q4_pack", "sgemv_q4_pack_gated", "sgemv_q4_desc_from_header", "sgemv_q4_run", "sgemv_q4_run_gated",
+            "sgemv_q4_pack", "sgemv_q4_pack_gated", "sgemv_q4_pack_device",
+            "sgemv_q4_desc_from_header", "sgemv_q4_run", "sgemv_q4_run_gated",
             "sgemv_block_norm",
             "sgemv_strerror", "sgemv_last_hip_error"]
 
@@ -113,6 +114,8 @@ def lib():
     L.sgemv_q4_pack.restype = ctypes.c_int
     L.sgemv_q4_pack_gated.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, u32, vp, sz, pq]
     L.sgemv_q4_pack_gated.restype = ctypes.c_int
+    L.sgemv_q4_pack_device.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, u32, vp, sz, pq, vp]
+    L.sgemv_q4_pack_device.restype = ctypes.c_int
     L.sgemv_q4_desc_from_header.argtypes = [vp, sz, pq]
     L.sgemv_q4_desc_from_header.restype = ctypes.c_int
     L.sgemv_q4_run.argtypes = [pq, vp, vp, i32, i32, i32, vp, vp, i32, i32, vp]
@@ -602,6 +605,43 @@ def sgemv_q4_pack_gated(gate, up, group: int = SGEMV_GROUP, bf16_scales: bool | 
     return d, blob
 
 
+def sgemv_q4_pack_device(q, scales, zeros=None, up=None, group: int = SGEMV_GROUP):
+    """sgemv_q4_pack (or, with up = (q, scales, zeros), sgemv_q4_pack_gated)
+    of torch tensors that are on one GPU, on that GPU and its current stream;
+    scales are float16 or bfloat16.  Codes, scales and zero-points are
+    checked, which waits for the GPU.  Returns (Q4Desc, uint8 GPU tensor)."""
+    _type_code(scales, "scales")
+    torch, parts = _torch, [(q, scales, zeros)] + ([] if up is None else [tuple(up)])
+    N, K = q.shape if q.dim() == 2 else (0, 0)
+    flags = (SGEMV_Q4_ZEROS if zeros is not None else 0) | (SGEMV_Q4_GATED if up is not None else 0) | \
+        (SGEMV_Q4_BF16_SCALES if scales.dtype == torch.bfloat16 else 0)
+    d, fn = Q4Desc(), lib().sgemv_q4_pack if up is None else lib().sgemv_q4_pack_gated
+    _check(fn(*[None] * (3 * len(parts)), N, K, group, flags, None, 0, ctypes.byref(d)), "sgemv_q4_pack_device(size)")
+    kept, device, G = [], q.device, -(-K // group)
+    for name, (pq, ps, pz) in zip(("weight", "up"), parts):
+        if (pz is None) != (zeros is None):
+            raise ValueError("gate and up must both have zero-points, or neither")
+        for what, t, dtypes, shape in ((f"{name} codes", pq, (torch.uint8,), (N, K)),
+                                       (f"{name} scales", ps, (scales.dtype,) if name == "up" else
+                                        (torch.float16, torch.bfloat16), (N, G)),
+                                       (f"{name} zeros", pz, (torch.uint8,), (N, G))):
+            if t is None:
+                kept.append(None)
+                continue
+            if t.dtype not in dtypes or tuple(t.shape) != shape:
+                raise ValueError(f"{what}: {str(t.dtype).replace('torch.', '')} {tuple(t.shape)}, expected "
+                                 f"{' or '.join(str(x).replace('torch.', '') for x in dtypes)} {shape}")
+            _on_one_gpu(device, (what,), (t,))
+            if not (bool(torch.isfinite(t).all()) if t.is_floating_point() else int(t.max()) <= 15):
+                raise SgemvError(SGEMV_EINVAL, f"sgemv_q4_pack_device: {what}")
+            kept.append(t.contiguous())
+    blob = torch.empty(d.total_bytes, dtype=torch.uint8, device=device)
+    ptrs = [0 if t is None else t.data_ptr() for t in kept] + [0] * (6 - len(kept))
+    _call(lib().sgemv_q4_pack_device, device, (*ptrs, N, K, group, flags, blob.data_ptr(), blob.numel(), d,
+                                               _stream_on(device, None)), "sgemv_q4_pack_device")
+    return d, blob
+
+
 def sgemv_q4_desc_from_header(blob) -> Q4Desc:
     b = np.ascontiguousarray(np.asarray(blob, dtype=np.uint8)[:256])
     d = Q4Desc()
@@ -794,15 +834,25 @@ class FusedProjections:
 class Q4Matrix:
     """A matrix (or gate/up pair) packed for sgemv_q4_run (sgemv_q4_run_gated)
     on the device: codes q uint8 [N][K], scales [N][ceil(K/group)], zeros
-    uint8 or None (symmetric)."""
+    uint8 or None (symmetric).  GPU tensors are packed on their GPU, host
+    arrays on the host."""
 
-    def __init__(self, q, scales, zeros=None, group: int = SGEMV_GROUP, device="cuda", bf16_scales=None, _packed=None):
+    def __init__(self, q, scales, zeros=None, group: int = SGEMV_GROUP, device="cuda", bf16_scales=None, _up=None):
         import torch
-        self.desc, blob = _packed or sgemv_q4_pack(q, scales, zeros, group, bf16_scales)
-        self.blob = torch.from_numpy(blob).to(device)
+        if isinstance(q, torch.Tensor) and q.is_cuda:
+            if bf16_scales not in (None, _is_bf16(scales)):
+                raise ValueError("scales on a GPU are float16 or bfloat16 tensors, which say their type themselves")
+            self.desc, blob = sgemv_q4_pack_device(q, scales, zeros, _up, group)
+        else:
+            if _up is None:
+                self.desc, blob = sgemv_q4_pack(q, scales, zeros, group, bf16_scales)
+            else:
+                self.desc, blob = sgemv_q4_pack_gated((q, scales, zeros), _up, group, bf16_scales)
+            blob = torch.from_numpy(blob)
+        self.blob = blob.to(device)
         self.N, self.K = self.desc.N, self.desc.K
 
     @classmethod
     def gated(cls, gate, up, group: int = SGEMV_GROUP, device="cuda", bf16_scales=None):
         """A gate and an up projection, each (q, scales, zeros)."""
-        return cls(None, None, device=device, _packed=sgemv_q4_pack_gated(gate, up, group, bf16_scales))
+        return cls(*gate, group=group, device=device, bf16_scales=bf16_scales, _up=tuple(up))

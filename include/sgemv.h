@@ -471,6 +471,21 @@ int sgemv_q4_pack_gated(const uint8_t* q_gate, const uint16_t* scales_gate,
                         int32_t N, int32_t K, int32_t group, uint32_t flags,
                         void* out, size_t out_capacity, sgemv_q4_desc* desc_out);
 
+/*
+ * sgemv_q4_pack_device - the same blob, byte for byte, made on the device from
+ * codes, scales and zero-points that are there already (the up projection's
+ * with SGEMV_Q4_GATED in flags, else NULL).
+ *   packed   device buffer of `capacity` bytes, 256-byte aligned (a size query
+ *            is sgemv_q4_pack or sgemv_q4_pack_gated with out == NULL)
+ * Shapes and types as above, in device memory.  Codes and zero-points are not
+ * checked: their low four bits are taken.  EINVAL, ESIZE and EALIGN as above.
+ */
+int sgemv_q4_pack_device(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros,
+                         const uint8_t* q_up, const uint16_t* scales_up,
+                         const uint8_t* zeros_up, int32_t N, int32_t K, int32_t group,
+                         uint32_t flags, void* packed, size_t capacity,
+                         sgemv_q4_desc* desc_out, void* stream);
+
 /* Parse and check the header (at least 80 bytes) of a blob of either call.
  * EINVAL on a bad magic, version or inconsistent fields. */
 int sgemv_q4_desc_from_header(const void* header, size_t bytes,

@@ -108,6 +108,57 @@ def test_product_larger(N, K, M, group, xt):
 
 
 @pytest.mark.parametrize("xt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,K,M,group", [(8300, 384, 3, 64), (8300, 384, 6, 32), (8300, 384, 16, 128), (16500, 300, 16, 32),
+                                         (16500, 1024, 9, 64), (33000, 640, 2, 32), (33000, 1000, 12, 128),
+                                         (5000, 4224, 16, 64), (300, 4224, 16, 32), (300, 8192, 8, 128)])
+def test_product_tiles_and_wavefronts(N, K, M, group, xt):
+    """Every number of tiles a workgroup has (1, 2, 4) and of wavefronts."""
+    check_product(N + K, N, K, M, group, xt, "f32", True, False, True)
+
+
+@pytest.mark.parametrize("M,xt", [(2, "f16"), (7, "bf16"), (16, "bf16"), (16, "f16")])
+@pytest.mark.parametrize("N,group", [(8200, 128), (20000, 32)])
+def test_product_streamed(N, M, xt, group):
+    """Matrices large enough for their codes to be read past the caches."""
+    K = -(-(96 << 21) // N // 128) * 128 + 37
+    gen = torch.Generator(device="cuda:0").manual_seed(N)
+    from activation_sparse_bit_amd import sgemv
+    g = -(-K // group)
+    q = torch.randint(0, 16, (N, K), dtype=torch.uint8, device="cuda:0", generator=gen)
+    s = (0.01 + 0.01 * torch.rand(N, g, device="cuda:0", generator=gen)).half()
+    z = torch.randint(0, 16, (N, g), dtype=torch.uint8, device="cuda:0", generator=gen)
+    m = sgemv.Q4Matrix(q, s, z, group=group)
+    assert m.desc.w_bytes >= 96 << 20
+    x = activations(5, M, K, xt)
+    y = torch.empty(M, N, dtype=torch.float32, device="cuda:0")
+    sgemv.sgemv_q4_run(m.desc, m.blob, x.cuda(), y)
+    rows = np.array(sorted({0, 1, 15, 16, 33, 63, 64, N // 2, N - 17, N - 2, N - 1}))
+    part = (q[rows].cpu().numpy(), s[rows].cpu(), z[rows].cpu().numpy())
+    ref = oracle.q4_product(f64(x), part[0], f64(part[1]), part[2], group)
+    check(y[:, rows], ref, accumulation(x, part, group) + rounding(ref, "f32") * 1.01, f"N={N} K={K}")
+
+
+@pytest.mark.parametrize("N,K,group", [(1, 1, 32), (16, 128, 128), (17, 129, 32), (100, 1000, 64), (333, 257, 128)])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_device_packer_makes_the_host_blob(N, K, group, zeros, bf16):
+    from activation_sparse_bit_amd import sgemv
+    a, b = problem(1, N, K, group, zeros, bf16), problem(2, N, K, group, zeros, bf16)
+    dev = lambda p: tuple(None if t is None else torch.as_tensor(t).cuda() for t in p)  # noqa: E731
+    for host, gpu in ((sgemv.sgemv_q4_pack(*a, group), sgemv.sgemv_q4_pack_device(*dev(a), group=group)),
+                      (sgemv.sgemv_q4_pack_gated(a, b, group), sgemv.sgemv_q4_pack_device(*dev(a), up=dev(b), group=group))):
+        assert host[0].as_dict() == gpu[0].as_dict()
+        assert np.array_equal(host[1], gpu[1].cpu().numpy())
+    q, s, z = dev(a)
+    q = q.clone(); q[-1, -1] = 16
+    with pytest.raises(sgemv.SgemvError):
+        sgemv.sgemv_q4_pack_device(q, s, z, group=group)
+    s = s.clone(); s[0, 0] = float("inf")
+    with pytest.raises(sgemv.SgemvError):
+        sgemv.sgemv_q4_pack_device(dev(a)[0], s, z, group=group)
+
+
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
 @pytest.mark.parametrize("off,pad", [(0, 5), (1, 0), (3, 7)])
 def test_strides_and_alignment(xt, off, pad):
     """Rows of a wider buffer at any element: x, bias and y start off a
@@ -207,6 +258,11 @@ def check_gated(seed, N, K, M, group, xt, ht, act, zeros=True, bias=False):
     ea = 1.13 * eg + 16 * 2.0 ** -24 * np.abs(g)
     tol = ea * (np.abs(u) + eu) + np.abs(oracle.gate_function(g, act)) * eu + 2.0 ** -23 * np.abs(ref)
     check(h[:M], ref, tol * (1 + 2.0 ** -7) + rounding(ref, ht) * (1 + 2.0 ** -7), f"{act} N={N} K={K} M={M}")
+
+
+@pytest.mark.parametrize("N,K,M,group,xt", [(8300, 384, 16, 64, "bf16"), (8300, 200, 11, 32, "f16"), (4200, 640, 2, 128, "f16")])
+def test_gated_tiles(N, K, M, group, xt):
+    check_gated(N, N, K, M, group, xt, "f32", "silu")
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu"])

@@ -200,6 +200,26 @@ def test_run_refusals():
     assert gated(bu=FAKE + 1) == E.SGEMV_EALIGN
 
 
+def test_device_packer_refusals():
+    L = sgemv.lib()
+
+    def pack(q=FAKE, s=FAKE, z=FAKE, qu=None, su=None, zu=None, N=16, K=128, group=64, flags=2, out=FAKE, cap=1 << 20):
+        return L.sgemv_q4_pack_device(q, s, z, qu, su, zu, N, K, group, flags, out, cap, None, None)
+
+    assert pack(q=None) == pack(s=None) == pack(z=None) == pack(out=None) == E.SGEMV_EINVAL
+    assert pack(group=48) == pack(flags=16) == pack(flags=3) == pack(flags=3, qu=FAKE, su=FAKE) == E.SGEMV_EINVAL
+    assert pack(N=0) == pack(K=1 << 17) == pack(cap=1791) == E.SGEMV_ESIZE   # 1792 needed
+    assert pack(out=FAKE + 16) == pack(s=FAKE + 1) == E.SGEMV_EALIGN
+    torch = pytest.importorskip("torch")
+    q, s, z = (torch.from_numpy(a) for a in problem(1, 16, 128, 64))
+    for match, f in (("GPU tensor", lambda: sgemv.sgemv_q4_pack_device(q, s, z, group=64)),
+                     ("codes", lambda: sgemv.sgemv_q4_pack_device(q.int(), s, z, group=64)),
+                     ("scales", lambda: sgemv.sgemv_q4_pack_device(q, s.float(), z, group=64)),
+                     ("both", lambda: sgemv.sgemv_q4_pack_device(q, s, z, up=(q, s, None), group=64))):
+        with pytest.raises(ValueError, match=match):
+            f()
+
+
 def norm_args(**kw):
     f = dict(rows=4, D=64, flags=0, residual=FAKE, y=0, gate=0, post_weight=0, post_bias=0, weight=0, bias=0,
              residual_out=0, x=FAKE + (1 << 16), ld_residual=64, ld_y=64, ld_gate=0, ld_residual_out=64, ld_x=64,
