@@ -617,7 +617,7 @@ def sgemv_q4_pack_device(q, scales, zeros=None, up=None, group: int = SGEMV_GROU
         (SGEMV_Q4_BF16_SCALES if scales.dtype == torch.bfloat16 else 0)
     d, fn = Q4Desc(), lib().sgemv_q4_pack if up is None else lib().sgemv_q4_pack_gated
     _check(fn(*[None] * (3 * len(parts)), N, K, group, flags, None, 0, ctypes.byref(d)), "sgemv_q4_pack_device(size)")
-    kept, device, G = [], q.device, -(-K // group)
+    device, G, operands = q.device, -(-K // group), []
     for name, (pq, ps, pz) in zip(("weight", "up"), parts):
         if (pz is None) != (zeros is None):
             raise ValueError("gate and up must both have zero-points, or neither")
@@ -625,16 +625,15 @@ def sgemv_q4_pack_device(q, scales, zeros=None, up=None, group: int = SGEMV_GROU
                                        (f"{name} scales", ps, (scales.dtype,) if name == "up" else
                                         (torch.float16, torch.bfloat16), (N, G)),
                                        (f"{name} zeros", pz, (torch.uint8,), (N, G))):
-            if t is None:
-                kept.append(None)
-                continue
-            if t.dtype not in dtypes or tuple(t.shape) != shape:
+            if t is not None and (t.dtype not in dtypes or tuple(t.shape) != shape):
                 raise ValueError(f"{what}: {str(t.dtype).replace('torch.', '')} {tuple(t.shape)}, expected "
                                  f"{' or '.join(str(x).replace('torch.', '') for x in dtypes)} {shape}")
-            _on_one_gpu(device, (what,), (t,))
-            if not (bool(torch.isfinite(t).all()) if t.is_floating_point() else int(t.max()) <= 15):
-                raise SgemvError(SGEMV_EINVAL, f"sgemv_q4_pack_device: {what}")
-            kept.append(t.contiguous())
+            operands.append((what, t))
+    _on_one_gpu(device, *zip(*operands))
+    for what, t in operands:
+        if t is not None and not (bool(torch.isfinite(t).all()) if t.is_floating_point() else int(t.max()) <= 15):
+            raise SgemvError(SGEMV_EINVAL, f"sgemv_q4_pack_device: {what}")
+    kept = [None if t is None else t.contiguous() for _, t in operands]
     blob = torch.empty(d.total_bytes, dtype=torch.uint8, device=device)
     ptrs = [0 if t is None else t.data_ptr() for t in kept] + [0] * (6 - len(kept))
     _call(lib().sgemv_q4_pack_device, device, (*ptrs, N, K, group, flags, blob.data_ptr(), blob.numel(), d,
