@@ -427,6 +427,12 @@ int run(const sgemv_q4_desc* d, const void* packed, const void* x, int x_type, i
     if (!aligned_to(packed, 256) || !aligned_to(x, 2) || !aligned_to(y, y_type == SGEMV_F32 ? 4 : 2) ||
         !aligned_to(bias0, 2) || !aligned_to(bias1, 2))
         return SGEMV_EALIGN;
+    const int ys = y_type == SGEMV_F32 ? 4 : 2;
+    const SgemvRows out{y, M, (int64_t)ldy * ys, (int64_t)d->N * ys};
+    if (sgemv_overlap(out, {x, M, (int64_t)ldx * 2, (int64_t)d->K * 2}) ||
+        sgemv_overlap(out, {packed, 1, 0, (int64_t)d->total_bytes}) ||
+        sgemv_overlap(out, {bias0, 1, 0, (int64_t)d->N * 2}) || sgemv_overlap(out, {bias1, 1, 0, (int64_t)d->N * 2}))
+        return SGEMV_EINVAL;
 
     const uint8_t* blob = static_cast<const uint8_t*>(packed);
     Q4Args a;

@@ -486,6 +486,8 @@ def _vector(t, what: str, n: int, code: int) -> int:
     """Address of an optional contiguous vector of at least n elements."""
     if t is None:
         return 0
+    if getattr(t, "shape", None) == (n,) and _TYPES.get(t.dtype) == code and t.is_contiguous():
+        return t.data_ptr()
     if _type_code(t, what) != code:
         raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')} differs from the operands it goes with")
     if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
@@ -650,6 +652,15 @@ def sgemv_q4_desc_from_header(blob) -> Q4Desc:
 
 def _q4_operands(desc, packed, x, y):
     """Checked (x type, rows, ldx, y type, ldy) of a q4 call."""
+    try:   # what nearly every call brings: two-dimensional operands, checked in few steps
+        xt, yt = _TYPES[x.dtype], _TYPES[y.dtype]
+        (M, k), (ldx, ex), (rows, n), (ldy, ey) = x.shape, x.stride(), y.shape, y.stride()
+        if (rows == M >= 1 and ex == 1 == ey and ldx >= k >= desc.K and ldy >= n >= desc.N and xt < SGEMV_F32
+                and (yt == xt or yt == SGEMV_F32) and packed.dtype is _torch.uint8 and packed.is_contiguous()
+                and packed.numel() >= desc.total_bytes):
+            return xt, M, ldx, yt, ldy
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
     xt, yt = _type_code(x, "x"), _type_code(y, "y")
     if xt == SGEMV_F32:
         raise ValueError("x: dtype float32, expected float16, bfloat16")
@@ -670,7 +681,7 @@ def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
     x's type or float32; bias is [N] of x's type.  Runs on `stream`, or on the
     current stream of the tensors' device."""
     xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y)
-    b = _vector(bias, "bias", desc.N, xt)
+    b = None if bias is None else _vector(bias, "bias", desc.N, xt)
     device = x.device
     _on_one_gpu(device, ("packed", "x", "y", "bias"), (packed, x, y, bias))
     _call(lib().sgemv_q4_run, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, b, y.data_ptr(), yt, ldy,
@@ -687,7 +698,8 @@ def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=
     if act not in _ACTS:
         raise ValueError(f"act: {act!r}, expected one of {', '.join(_ACTS)}")
     xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h)
-    bg, bu = _vector(bias_gate, "bias_gate", desc.N, xt), _vector(bias_up, "bias_up", desc.N, xt)
+    bg = None if bias_gate is None else _vector(bias_gate, "bias_gate", desc.N, xt)
+    bu = None if bias_up is None else _vector(bias_up, "bias_up", desc.N, xt)
     device = x.device
     _on_one_gpu(device, ("packed", "x", "h", "bias_gate", "bias_up"), (packed, x, h, bias_gate, bias_up))
     _call(lib().sgemv_q4_run_gated, device, (desc, packed.data_ptr(), x.data_ptr(), xt, M, ldx, bg, bu, _ACTS[act],
@@ -728,6 +740,8 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
             raise ValueError("gate: needs y, and y's type")
         if gate.dim() == 1:
             gp = _vector(gate, "gate", D, yt)
+        elif gate.shape[0] == rows and gate.stride(0) == 0:   # one vector, expanded
+            gp = _vector(gate[0], "gate", D, yt)
         else:
             ldg, gp = _row_stride(gate, "gate", rows, D), gate.data_ptr()
     wt, w0, w1, w2, w3 = -1, 0, 0, 0, 0

@@ -499,8 +499,8 @@ int sgemv_q4_desc_from_header(const void* header, size_t bytes,
  *   packed  device blob, 256-byte aligned
  *   x       device [M][ldx] of x_type: SGEMV_F16 or SGEMV_BF16
  *   bias    device [N] of x_type, or NULL
- *   y       device [M][ldy] of y_type: x_type or SGEMV_F32; must not overlap
- *           the inputs
+ *   y       device [M][ldy] of y_type: x_type or SGEMV_F32; refused where it
+ *           overlaps an input (columns of one wider buffer do not)
  *   ldx, ldy  row strides in elements, >= K and >= N.  Pointers need the
  *           alignment of their elements only.
  * Products are exact and sums are held in fp32, one group of inputs at a
@@ -510,9 +510,10 @@ int sgemv_q4_desc_from_header(const void* header, size_t bytes,
  * fit bf16's mantissa, and CDNA4 has no packed bf16 subtraction) and
  * (z + 16) * sum x is taken off each group's sum in fp32: the accumulation
  * error is relative to sum |s| (q + 16) |x| instead, at most a few 2^-24 of
- * it per group, and a row with an infinity gives NaN.
- * EINVAL for NULL, a bad type or description; ESIZE for M, ldx or ldy;
- * EALIGN for pointers.
+ * it per group, and a row with an infinity, or with values whose 32-fold sum
+ * over a group leaves fp32, gives NaN.
+ * EINVAL for NULL, a bad type or description or an overlap; ESIZE for M, ldx
+ * or ldy; EALIGN for pointers.
  */
 int sgemv_q4_run(const sgemv_q4_desc* d, const void* packed, const void* x,
                  int32_t x_type, int32_t M, int32_t ldx, const void* bias,
@@ -579,8 +580,9 @@ typedef struct sgemv_norm {
  *
  * Row strides are at least D and pointers need the alignment of their
  * elements only.  An output may be the very buffer of residual, y or a
- * per-row gate (same address, row stride and element size); any other
- * overlap of an output with another buffer is refused.
+ * per-row gate (same address, row stride and element size), and columns of one
+ * wider buffer may be different operands; any other meeting of an output's
+ * byte range with another buffer's is refused.
  * EINVAL for NULL residual or x, a bad flag, type, eps or overlap; ESIZE for
  * rows, D or a stride; EALIGN for pointers.
  */

@@ -135,6 +135,25 @@ def test_row_counts(rows):
     check(rows, rows, 640, "f16", "f32", "f16", "f16")
 
 
+@pytest.mark.parametrize("rows,D", [(513, 1032), (600, 1100), (700, 4099), (520, 8193), (300, 9000), (260, 16390),
+                                    (257, 12288), (512, 8200), (20, 20001), (9, 33000), (600, 8191)])
+@pytest.mark.parametrize("center", [False, True])
+def test_many_rows_and_widths(rows, D, center):
+    """Every number of runs a thread has, with and without odd elements."""
+    check(rows + D, rows, D, "bf16", "f32" if D % 2 else "bf16", "bf16", "f32", post=True, gate="rows", scale=0.5,
+          center=center, bias=True)
+
+
+def test_expanded_gate():
+    from activation_sparse_bit_amd import sgemv
+    p = make(3, 5, 200, "f16", "f16", "f16", "f16", False, "vector", False, False, False)
+    out = [torch.empty_like(p["residual"]) for _ in range(2)]
+    for x, g in zip(out, (p["gate"], p["gate"].expand(5, 200))):
+        sgemv.sgemv_block_norm(x, p["residual"], p["y"], weight=p["weight"], gate=g)
+    torch.cuda.synchronize()
+    assert torch.equal(*out)
+
+
 def test_no_rows():
     from activation_sparse_bit_amd import sgemv
     x, r = torch.empty(0, 64, device="cuda:0"), torch.empty(0, 64, device="cuda:0")

@@ -179,6 +179,20 @@ def test_strides_and_alignment(xt, off, pad):
     assert (out[:, :1] == 7).all() and (out[:, 1 + N:] == 7).all()
 
 
+def test_operands_in_one_buffer():
+    """x and y as columns of one wider buffer."""
+    from activation_sparse_bit_amd import sgemv
+    part = problem(15, 70, 200, 64)
+    x = activations(16, 5, 200, "f16")
+    m = sgemv.Q4Matrix(*part, group=64, device="cuda:0")
+    wide = torch.full((5, 300), 3.0, dtype=torch.float16, device="cuda:0")
+    wide[:, 75:275] = x.cuda()
+    sgemv.sgemv_q4_run(m.desc, m.blob, wide[:, 75:275], wide[:, 3:73])
+    ref = oracle.q4_product(f64(x), part[0], f64(part[1]), part[2], 64)
+    check(wide[:, 3:73], ref, accumulation(x, part, 64) + rounding(ref, "f16") * 1.01)
+    assert torch.equal(wide[:, 75:275].cpu(), x) and (wide[:, :3] == 3).all() and (wide[:, 275:] == 3).all()
+
+
 def test_codes_equal_to_zero_points_give_zero():
     """q = z everywhere: exactly 0 for fp16 activations; for bf16 the sums of
     (16 + z) x and their correction cancel to accumulation error."""

@@ -187,6 +187,11 @@ def test_run_refusals():
     assert run(M=0) == run(M=17) == run(M=-1) == run(ldx=199) == run(ldy=39) == E.SGEMV_ESIZE
     assert run(packed=FAKE + 128) == run(x=FAKE + 1) == run(y=FAKE + 1) == run(y=FAKE + 2, yt=2) == E.SGEMV_EALIGN
     assert run(bias=FAKE + 1) == E.SGEMV_EALIGN
+    # y inside x's rows, x inside y's, y over the blob or the bias, columns that meet
+    assert run(packed=FAKE << 2, y=FAKE + 398) == run(packed=FAKE << 2, x=FAKE + 78) == E.SGEMV_EINVAL
+    assert run(y=FAKE + int(d.total_bytes) - 2, x=FAKE << 2) == run(packed=FAKE << 2, x=FAKE << 3, bias=FAKE) == E.SGEMV_EINVAL
+    assert run(packed=FAKE << 2, M=4, ldx=512, ldy=512, y=FAKE + 398) == E.SGEMV_EINVAL
+    assert run(packed=FAKE << 2, M=4, ldx=512, ldy=512, y=FAKE + 1024 - 78) == E.SGEMV_EINVAL
     bad = E.Q4Desc(**d.as_dict()); bad.s_off += 256
     assert run(d=bad) == E.SGEMV_EINVAL
     bad = E.Q4Desc(**d.as_dict()); bad.K = 0
