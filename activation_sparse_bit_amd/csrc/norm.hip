@@ -461,11 +461,12 @@ extern "C" int sgemv_block_norm(const sgemv_norm* args, void* stream) {
         k = pick<true, 1>(rb, yb, odd);
         rows_per = 4;
     } else {
-        // Runs a thread.  One is fastest for a few rows, where only latency counts (16 x 4096: 4.4 us, 5.4 with two);
-        // many rows want several runs in flight a thread and room for more rows on a compute unit (8192 x 4096: 53 us
-        // with two runs, 67 with one, 65 with four; 2048 x 14336: 65 us with four, 70 with two).
+        // Runs a thread.  One is fastest for a few rows, where only latency counts (16 x 5001: 4.8 us, 5.7 with two;
+        // 16 x 14336, too long for one: 5.7 with two, 7.4 with four); many long rows want several runs in flight a
+        // thread and room for more rows on a compute unit (8192 x 8192: 104 us with two runs, 112 with one, 115 with
+        // four; 512 x 14336: 14.4 us with four, 16.8 with two).
         int CH = 1;
-        if (runs > 512 || (runs > 128 && a.rows > 512)) CH = 2;
+        if (runs > 1024 || (runs > 512 && a.rows > 256) || (runs > 256 && a.rows > 512)) CH = 2;
         if (runs > 2048 || (runs > 1024 && a.rows > 256)) CH = 4;
         if (runs > 4096) CH = 8;
         block = (unsigned)((runs + CH * 64 - 1) / (CH * 64) * 64);

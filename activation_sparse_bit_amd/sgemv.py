@@ -710,24 +710,13 @@ def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=
 _NORM = struct.Struct("@qiI9P5q2f4i")
 
 
-def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bias=None, post_weight=None,
-                     post_bias=None, gate=None, scale: float = 1.0, eps: float = 1e-6, post_norm: bool | None = None,
-                     center: bool = False, plus_one: bool = False, stream=None):
-    """From a block's output y to the next block's input, in one launch:
-    r = residual + scale * gate * u with u = y, or norm(y; post_weight,
-    post_bias) when post_norm (by default: when either is given);
-    residual_out (optional) receives r, x receives norm(r; weight, bias).
-    The norm is the root mean square norm, or layer norm with center;
-    plus_one takes weights stored around zero.  x, residual, y, residual_out
-    are [D] or [rows][>= D] in float16, bfloat16 or float32 (residual_out of
-    residual's type); gate is [D] or [rows][D] of y's type; the vectors share
-    one type.  D is residual's last dimension; residual_out may be residual
-    and x may be y."""
+def _norm_operands(x, residual, y, residual_out, weight, bias, post_weight, post_bias, gate):
+    """Checked (rows, D, addresses, strides, types) of a sgemv_block_norm call."""
     rt, xt = _type_code(residual, "residual"), _type_code(x, "x")
     rows = 1 if residual.dim() == 1 else residual.shape[0]
     D = residual.shape[-1] if residual.dim() else 0
     ldr, ldx = _row_stride(residual, "residual", rows, D), _row_stride(x, "x", rows, D)
-    device, flags = residual.device, 0
+    device = residual.device
     yt, ldy, yp, ldg, gp, ldo, op = rt, 0, 0, 0, 0, 0, 0
     if y is not None:
         yt, ldy, yp = _type_code(y, "y"), _row_stride(y, "y", rows, D), y.data_ptr()
@@ -757,6 +746,65 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
     if post_bias is not None:
         wt = _type_code(post_bias, "post_bias") if wt < 0 else wt
         w1 = _vector(post_bias, "post_bias", D, wt)
+    _on_one_gpu(device, ("residual", "x", "y", "residual_out", "gate", "weight", "bias", "post_weight", "post_bias"),
+                (residual, x, y, residual_out, gate, weight, bias, post_weight, post_bias))
+    return (rows, D, (residual.data_ptr(), yp, gp, w0, w1, w2, w3, op, x.data_ptr()), (ldr, ldy, ldg, ldo, ldx),
+            (rt, yt, wt if wt >= 0 else xt, xt))
+
+
+def _norm_operands_quick(x, residual, y, residual_out, vectors, gate):
+    """The same in few steps for what nearly every call brings (matrices of
+    two dimensions, vectors of D elements), or None."""
+    rt, xt = _TYPES[residual.dtype], _TYPES[x.dtype]
+    (rows, D), (ldr, e), device = residual.shape, residual.stride(), residual.device
+    (r, n), (ldx, ex) = x.shape, x.stride()
+    if not (e == 1 == ex and r == rows and ldr >= D and ldx >= n >= D and x.device == device and device.type == "cuda"):
+        return None
+    yt, ldy, yp, gp, ldg, ldo, op, wt, wp = rt, 0, 0, 0, 0, 0, 0, xt, []
+    if y is not None:
+        (r, n), (ldy, e), yt, yp = y.shape, y.stride(), _TYPES[y.dtype], y.data_ptr()
+        if not (e == 1 and r == rows and ldy >= n >= D and y.device == device):
+            return None
+    if residual_out is not None:
+        (r, n), (ldo, e), op = residual_out.shape, residual_out.stride(), residual_out.data_ptr()
+        if not (e == 1 and r == rows and ldo >= n >= D and residual_out.device == device
+                and residual_out.dtype is residual.dtype):
+            return None
+    if gate is not None:
+        if y is None or gate.dtype is not y.dtype or not gate.is_contiguous() or gate.device != device:
+            return None
+        gp = gate.data_ptr()
+        if gate.shape == (rows, D):
+            ldg = D
+        elif gate.shape != (D,):
+            return None
+    dtype = None
+    for w in vectors:
+        if w is None:
+            wp.append(0)
+            continue
+        if dtype is None:
+            dtype, wt = w.dtype, _TYPES[w.dtype]
+        if w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous() or w.device != device:
+            return None
+        wp.append(w.data_ptr())
+    return (rows, D, (residual.data_ptr(), yp, gp, *wp, op, x.data_ptr()), (ldr, ldy, ldg, ldo, ldx), (rt, yt, wt, xt))
+
+
+def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bias=None, post_weight=None,
+                     post_bias=None, gate=None, scale: float = 1.0, eps: float = 1e-6, post_norm: bool | None = None,
+                     center: bool = False, plus_one: bool = False, stream=None):
+    """From a block's output y to the next block's input, in one launch:
+    r = residual + scale * gate * u with u = y, or norm(y; post_weight,
+    post_bias) when post_norm (by default: when either is given);
+    residual_out (optional) receives r, x receives norm(r; weight, bias).
+    The norm is the root mean square norm, or layer norm with center;
+    plus_one takes weights stored around zero.  x, residual, y, residual_out
+    are [D] or [rows][>= D] in float16, bfloat16 or float32 (residual_out of
+    residual's type); gate is [D] or [rows][D] of y's type; the vectors share
+    one type.  D is residual's last dimension; residual_out may be residual
+    and x may be y."""
+    flags = 0
     if post_norm is None:
         post_norm = post_weight is not None or post_bias is not None
     if post_norm:
@@ -769,10 +817,15 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
         flags |= SGEMV_NORM_CENTER
     if plus_one:
         flags |= SGEMV_NORM_PLUS_ONE
-    _on_one_gpu(device, ("residual", "x", "y", "residual_out", "gate", "weight", "bias", "post_weight", "post_bias"),
-                (residual, x, y, residual_out, gate, weight, bias, post_weight, post_bias))
-    args = _NORM.pack(rows, D, flags, residual.data_ptr(), yp, gp, w0, w1, w2, w3, op, x.data_ptr(), ldr, ldy, ldg,
-                      ldo, ldx, scale, eps, rt, yt, wt if wt >= 0 else xt, xt)
+    try:
+        found = _norm_operands_quick(x, residual, y, residual_out, (post_weight, post_bias, weight, bias), gate)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        found = None
+    if found is None:
+        found = _norm_operands(x, residual, y, residual_out, weight, bias, post_weight, post_bias, gate)
+    rows, D, addresses, strides, types = found
+    device = residual.device
+    args = _NORM.pack(rows, D, flags, *addresses, *strides, scale, eps, *types)
     _call(lib().sgemv_block_norm, device, (args, _stream_on(device, stream)), "sgemv_block_norm")
 
 
