@@ -10,9 +10,13 @@
 // one output, and a lane of the result holds that same output, so a lane
 // needs the scale and the zero-point of one output only.
 //
-// Row m of x is row (m % 4) * 4 + m / 4 of its operand: result register i of
-// a lane then is row lane / 16 + 4 i, and with at most four rows only the
-// first of the four result registers is scaled and summed.
+// Up to four rows: operand row 4 r + j holds row r's inputs of step j, so one
+// 16-byte load a lane brings what four steps need; step j's products are read
+// from result register j.  Up to eight rows two steps share a load, up to
+// sixteen each step has its own.  Activations are read in row order and put
+// into operand order through the wavefront's own LDS: loaded directly, the 64
+// lanes of a load would touch 64 pieces in 16 lines (28672 x 8192 gated, 16
+// rows: 62 us instead of 58).
 //
 // fp16 activations: codes become exact fp16 integers q - z (bits 0x6400 | q
 // are 1024 + q, and (1024 + 16 q) / 16 - 64 for the upper nibbles).  bf16
@@ -23,6 +27,14 @@
 // their sums in registers, and add them over LDS in wavefront order, so there
 // is nothing to hand from one workgroup to another and the result does not
 // depend on timing.
+//
+// Bound by HBM where the matrix is large: 100003 x 4096 (four rows, 219 MB) in
+// 36 us, 6.0 TB/s, the vector units 80 % busy; 28672 x 8192 gated (16 rows, 251
+// MB) in 54 us.  With sixteen rows the L2 counts too: 8192 x 28672 (123 MB) in
+// 32 us, its activations read 256 times (235 MB).  A small one (2048 x 2048, 3.1
+// us) is launch and latency.  Many resident wavefronts hide the latency, not
+// prefetching: two blocks in flight a wavefront cost registers and gained 3 %
+// at most.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
