@@ -17,8 +17,8 @@ struct SgemvRows {
 inline bool sgemv_overlap(const SgemvRows& a, const SgemvRows& b) {
     if (!a.p || !b.p) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    const uintptr_t a1 = a0 + (uintptr_t)((a.rows - 1) * a.step + a.len);
-    const uintptr_t b1 = b0 + (uintptr_t)((b.rows - 1) * b.step + b.len);
+    const uintptr_t a1 = a0 + (uintptr_t)(a.rows - 1) * (uintptr_t)a.step + (uintptr_t)a.len;
+    const uintptr_t b1 = b0 + (uintptr_t)(b.rows - 1) * (uintptr_t)b.step + (uintptr_t)b.len;
     if (a1 <= b0 || b1 <= a0) return false;
     if (a.rows > 1 && b.rows > 1 && a.step == b.step) {
         const uintptr_t step = (uintptr_t)a.step, off = b0 > a0 ? (b0 - a0) % step : (step - (a0 - b0) % step) % step;

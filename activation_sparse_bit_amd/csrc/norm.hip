@@ -479,9 +479,23 @@ extern "C" int sgemv_block_norm(const sgemv_norm* args, void* stream) {
             : CH == 4 ? pick<false, 4>(rb, yb, odd)
                       : pick<false, 8>(rb, yb, odd);
     }
-    void* kargs[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k),
-                                         dim3((unsigned)((a.rows + rows_per - 1) / rows_per)), dim3(block), kargs, 0,
-                                         static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? SGEMV_OK : sgemv_hip_failed((int)e);
+    // A launch has fewer than 2^32 threads: many rows take several, of 2^21 rows each.
+    const int64_t all = a.rows, most = (int64_t)1 << 21;
+    const auto advance = [&](const void* p, int64_t ld, int size) -> const void* {
+        return p ? static_cast<const uint8_t*>(p) + most * ld * size : nullptr;
+    };
+    for (int64_t done = 0; done < all; done += most) {
+        a.rows = all - done < most ? all - done : most;
+        void* kargs[] = {&a};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k),
+                                             dim3((unsigned)((a.rows + rows_per - 1) / rows_per)), dim3(block), kargs, 0,
+                                             static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return sgemv_hip_failed((int)e);
+        a.residual = advance(a.residual, a.ld_residual, rb);
+        a.y = advance(a.y, a.ld_y, yb);
+        a.gate = advance(a.gate, a.ld_gate, yb);
+        a.residual_out = const_cast<void*>(advance(a.residual_out, a.ld_residual_out, rb));
+        a.x = const_cast<void*>(advance(a.x, a.ld_x, xb));
+    }
+    return SGEMV_OK;
 }

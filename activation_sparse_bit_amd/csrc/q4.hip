@@ -333,14 +333,13 @@ struct PackArgs {
     sgemv_q4_desc d;
 };
 
-// A thread writes 16 bytes: the codes of one lane in one cell, the header,
+// Sixteen bytes of the blob: the codes of one lane in one cell, the header,
 // or scales and zero-points.  Bound by reading a byte a code; rows are read
 // in pieces of eight bytes, which the caches put together.
-__global__ __launch_bounds__(256) void k_q4_pack(PackArgs a) {
+__device__ __forceinline__ void pack_16(const PackArgs& a, uint64_t id) {
     const uint64_t blocks = (a.d.K + kBlockK - 1) / kBlockK, parts = (a.d.flags & SGEMV_Q4_GATED) ? 2 : 1;
     const uint64_t slots = a.d.w_bytes / 16, P = kBlockK / a.d.group;
     const uint64_t N = a.d.N, K = a.d.K, G = (K + a.d.group - 1) / a.d.group;
-    const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
     if (id < slots) {
         const uint64_t cell = id >> 6, r = id & 15, c = id >> 4 & 3;
         const uint64_t b = cell % blocks, tile = cell / blocks, n = tile / parts * kTileN + r;
@@ -393,6 +392,10 @@ __global__ __launch_bounds__(256) void k_q4_pack(PackArgs a) {
         byte[i] = (uint8_t)v;
     }
     for (int i = 0; i < 16; ++i) a.blob[at + i] = byte[i];
+}
+
+__global__ __launch_bounds__(256) void k_q4_pack(PackArgs a, uint64_t n) {
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (uint64_t)gridDim.x * 256) pack_16(a, id);
 }
 
 typedef void (*Kernel)(Q4Args);
@@ -536,9 +539,10 @@ extern "C" int sgemv_q4_pack_device(const uint8_t* q, const uint16_t* scales, co
     a.z[0] = zeros;
     a.z[1] = zeros_up;
     a.blob = static_cast<uint8_t*>(packed);
-    const uint64_t threads = a.d.w_bytes / 16 + 16 + (a.d.total_bytes - a.d.s_off + 15) / 16;
-    void* args[] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k_q4_pack), dim3((unsigned)((threads + 255) / 256)),
+    uint64_t n = a.d.w_bytes / 16 + 16 + (a.d.total_bytes - a.d.s_off + 15) / 16;
+    const uint64_t grid = (n + 255) / 256, most = 1u << 22;   // a launch has fewer than 2^32 threads
+    void* args[] = {&a, &n};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k_q4_pack), dim3((unsigned)(grid < most ? grid : most)),
                                          dim3(256), args, 0, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return sgemv_hip_failed((int)e);
     if (desc_out) *desc_out = a.d;

@@ -566,7 +566,7 @@ typedef struct sgemv_norm {
 
 /*
  * sgemv_block_norm - from the output y of one block to the input x of the
- * next, in one launch, one pass over the rows:
+ * next, in one pass over the rows (one launch for up to 2^21 of them):
  *   u  = y, or norm(y; post_weight, post_bias) with SGEMV_NORM_POST
  *   r  = residual + scale * gate * u      (gate 1 when NULL)
  *   residual_out = r

@@ -144,6 +144,25 @@ def test_many_rows_and_widths(rows, D, center):
           center=center, bias=True)
 
 
+@pytest.mark.parametrize("D", [8, 11])
+def test_more_rows_than_a_launch_takes(D):
+    """More than 2^21 rows: two launches; the last rows as one call has them."""
+    from activation_sparse_bit_amd import sgemv
+    rows, n = (1 << 21) + 6, 9
+    gen = torch.Generator(device="cuda:0").manual_seed(D)
+    r = torch.randn(rows, D, device="cuda:0", generator=gen).half()
+    y = torch.randn(rows, D, device="cuda:0", generator=gen).bfloat16()
+    gate = torch.rand(rows, D, device="cuda:0", generator=gen).bfloat16()
+    x, ro = torch.full((rows + 1, D), 7.0, device="cuda:0"), torch.empty_like(r)
+    sgemv.sgemv_block_norm(x[:rows], r, y, ro, gate=gate, post_norm=True)
+    for a, b in ((0, n), ((1 << 21) - 4, (1 << 21) + 6)):
+        want, want_r = torch.empty(b - a, D, device="cuda:0"), torch.empty(b - a, D, device="cuda:0").half()
+        sgemv.sgemv_block_norm(want, r[a:b], y[a:b], want_r, gate=gate[a:b], post_norm=True)
+        torch.cuda.synchronize()
+        assert torch.equal(x[a:b], want) and torch.equal(ro[a:b], want_r)
+    assert (x[rows] == 7).all()
+
+
 def test_expanded_gate():
     from activation_sparse_bit_amd import sgemv
     p = make(3, 5, 200, "f16", "f16", "f16", "f16", False, "vector", False, False, False)
