@@ -144,6 +144,20 @@ def test_many_rows_and_widths(rows, D, center):
           center=center, bias=True)
 
 
+@pytest.mark.parametrize("seed", range(80))
+def test_random_combinations(seed):
+    rng = np.random.default_rng(7000 + seed)
+    pick = lambda *a: a[int(rng.integers(len(a)))]  # noqa: E731
+    size = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))  # noqa: E731
+    D = size(1, 40000)
+    rows = size(1, max(2, min(1500, (1 << 21) // D)))
+    y = pick("f16", "bf16", "f32", None)
+    flag = lambda p: bool(rng.random() < p)  # noqa: E731
+    check(7000 + seed, rows, D, pick(*T), y, pick(*T), pick("f16", "bf16", "f32", None), post=y is not None and flag(0.5),
+          gate=None if y is None else pick(None, "vector", "rows"), scale=pick(1.0, 0.5, -0.3), center=flag(0.4),
+          plus_one=flag(0.3), bias=flag(0.5), eps=pick(1e-5, 1e-3), r_out=flag(0.8))
+
+
 @pytest.mark.parametrize("D", [8, 11])
 def test_more_rows_than_a_launch_takes(D):
     """More than 2^21 rows: two launches; the last rows as one call has them."""

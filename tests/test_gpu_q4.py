@@ -303,6 +303,20 @@ def test_gated_saturates():
         assert (h[0, :16] == 700.0 * 100.0).all() and (h[0, 16:] == 0).all()
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_random_combinations(seed):
+    rng = np.random.default_rng(9000 + seed)
+    pick = lambda *a: a[int(rng.integers(len(a)))]  # noqa: E731
+    size = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))  # noqa: E731
+    N, K, M, group, xt = size(1, 3000), size(1, 6000), int(rng.integers(1, 17)), pick(32, 64, 128), pick("f16", "bf16")
+    zeros, bias = bool(rng.random() < 0.6), bool(rng.random() < 0.5)
+    if rng.random() < 0.4:
+        check_gated(9000 + seed, min(N, 1500), K, M, group, xt, pick(xt, "f32"), pick("silu", "gelu", "relu"), zeros, bias)
+    else:
+        check_product(9000 + seed, N, K, M, group, xt, pick(xt, "f32"), zeros, bool(rng.random() < 0.4), bias,
+                      pick(None, N + int(rng.integers(1, 40))))
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, offsets
 # ---------------------------------------------------------------------------
