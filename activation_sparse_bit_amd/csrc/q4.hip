@@ -30,7 +30,7 @@
 //
 // Bound by HBM where the matrix is large: 100003 x 4096 (four rows, 219 MB) in
 // 36 us, 6.0 TB/s, the vector units 80 % busy; 28672 x 8192 gated (16 rows, 251
-// MB) in 54 us.  With sixteen rows the L2 counts too: 8192 x 28672 (123 MB) in
+// MB) in 52 us.  With sixteen rows the L2 counts too: 8192 x 28672 (123 MB) in
 // 32 us, its activations read 256 times (235 MB).  A small one (2048 x 2048, 3.1
 // us) is launch and latency.  Many resident wavefronts hide the latency, not
 // prefetching: two blocks in flight a wavefront cost registers and gained 3 %
@@ -68,7 +68,7 @@ struct Q4Args {
     int32_t blocks;      // blocks of 128 inputs
     int32_t gated, act;
     int32_t x_bf16, y_f32, s_bf16;
-    uint32_t z_stride, z_mask, z_set;
+    uint32_t z_stride;   // 0: no zero-points, all 8
 };
 
 __device__ __forceinline__ float bf16_f32(uint32_t b) { return __builtin_bit_cast(float, b << 16); }
@@ -77,19 +77,27 @@ __device__ __forceinline__ float f16_f32(uint32_t b) { return (float)__builtin_b
 // Masks and exponents of the unpacking, in registers that the compiler takes
 // as unknown: with literals it emits an AND and an OR where one v_and_or_b32
 // does (a third of the unpacking).
+template <bool Z_IN_VECTOR>
 struct Unpack {
-    uint32_t lo, hi, exp;
-    __device__ __forceinline__ Unpack(bool bf) : lo(bf ? 0x00780078u : 0x000F000Fu), hi(0x00F000F0u),
-                                                 exp(bf ? 0x41804180u : 0x64006400u) {
+    uint32_t lo, hi, exp, z_mask, z_exp;   // codes; zero-points: without any, the mask is 0 and the 8 in z_exp
+    __device__ __forceinline__ Unpack(bool bf, bool zeros)
+        : lo(bf ? 0x00780078u : 0x000F000Fu), hi(0x00F000F0u), exp(bf ? 0x41804180u : 0x64006400u),
+          z_mask(!zeros ? 0u : bf ? 15u << 19 : 15u),
+          z_exp((bf ? 0x41800000u : 0x6400u) | (zeros ? 0u : bf ? 8u << 19 : 8u)) {
         asm("" : "+s"(lo));
         asm("" : "+s"(hi));
         asm("" : "+v"(exp));
+        // one v_and_or_b32 for a zero-point too, where it shows: several groups a block, or bf16 (28672 x 8192 gated, 16
+        // rows: 53.2 -> 51.4 us); with one group and fp16 the scalar form is as fast or faster (12.7 against 12.9)
+        if constexpr (Z_IN_VECTOR) asm("" : "+v"(z_exp));
+        else asm("" : "+s"(z_exp));
     }
 };
 
 // One word of eight codes as the fp16 integers q - z; zl is 1024 + z and zh
 // is 64 + z, twice each.
-__device__ __forceinline__ half8_t unpack_f16(const Unpack& u, uint32_t w, half2_t zl, half2_t zh) {
+template <class U>
+__device__ __forceinline__ half8_t unpack_f16(const U& u, uint32_t w, half2_t zl, half2_t zh) {
     const half2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     half2_t p[4];
     p[0] = __builtin_bit_cast(half2_t, (w & u.lo) | u.exp) - zl;
@@ -101,7 +109,8 @@ __device__ __forceinline__ half8_t unpack_f16(const Unpack& u, uint32_t w, half2
 }
 
 // The same as the bf16 integers q + 16.
-__device__ __forceinline__ bf8_t unpack_bf16(const Unpack& u, uint32_t w) {
+template <class U>
+__device__ __forceinline__ bf8_t unpack_bf16(const U& u, uint32_t w) {
     uint4_t v;
     v[0] = ((w << 3) & u.lo) | u.exp;
     v[1] = ((w >> 1) & u.lo) | u.exp;
@@ -137,8 +146,10 @@ struct Meta {
         const float f = f16_f32(b & 0xFFFFu), h = bf16_f32(b);
         return bf16 ? h : f;
     }
-    __device__ __forceinline__ uint32_t zero(const Q4Args& a, int g, int n16) const {
-        return ((z >> ((n16 * P & 7) * 4 + g * 4)) & a.z_mask) | a.z_set;   // masks 15 and 0, or 0 and 8
+    // The zero-point's nibble moved to bit `to` of the word.
+    __device__ __forceinline__ uint32_t moved(int g, int n16, int to) const {
+        const int at = (n16 * P & 7) * 4 + g * 4;
+        return to ? __builtin_amdgcn_alignbit(z, z, (at - to) & 31) : z >> at;
     }
 };
 
@@ -187,7 +198,7 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
             md[t].load(a, cell[t] + b, n16);
         }
     };
-    const Unpack u(BF);
+    const Unpack<BF || (P > 1)> u(BF, a.z_stride != 0);
     const auto multiply = [&](const uint4_t (&w)[NT], const Meta<P> (&md)[NT], const uint4_t (&raw)[MR]) {
         // From rows to operands through the wavefront's own LDS (its accesses are in order; the fences hold the
         // compiler to it).
@@ -222,9 +233,10 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float s = md[t].scale(g, n16, a.s_bf16);
-                const uint32_t z = md[t].zero(a, g, n16);
-                const half2_t zl = __builtin_bit_cast(half2_t, (0x6400u | z) * 0x10001u);   // 1024 + z
-                const half2_t zh = zl - half2_t{(_Float16)960.0f, (_Float16)960.0f};        // 64 + z
+                // 16 + z in fp32 for bf16 activations; 1024 + z and 64 + z in fp16, twice each, for fp16
+                const uint32_t zb = (md[t].moved(g, n16, BF ? 19 : 0) & u.z_mask) | u.z_exp;
+                const half2_t zl = __builtin_bit_cast(half2_t, zb << 16 | zb);
+                const half2_t zh = zl - half2_t{(_Float16)960.0f, (_Float16)960.0f};
                 float4_t acc[kPhases];
 #pragma unroll
                 for (int q = 0; q < kPhases; ++q) acc[q] = float4_t{0, 0, 0, 0};
@@ -244,7 +256,7 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
                     float v = acc[0][i * J + g * kSteps % J];
 #pragma unroll
                     for (int q = 1; q < kPhases; ++q) v += acc[q][i * J + (g * kSteps + q) % J];
-                    if constexpr (BF) v = fmaf(-(float)(16u + z), ones[i], v);
+                    if constexpr (BF) v = fmaf(-__builtin_bit_cast(float, zb), ones[i], v);
                     sum[t][i] = fmaf(s, v, sum[t][i]);
                 }
             }
@@ -457,8 +469,6 @@ int run(const sgemv_q4_desc* d, const void* packed, const void* x, int x_type, i
     const bool zeros = (d->flags & SGEMV_Q4_ZEROS) != 0;
     a.z = zeros ? blob + d->z_off : a.s;
     a.z_stride = zeros ? kTileN / 2 * (kBlockK / d->group) : 0;
-    a.z_mask = zeros ? 15 : 0;
-    a.z_set = zeros ? 0 : 8;
     a.x = static_cast<const uint16_t*>(x);
     a.bias[0] = static_cast<const uint16_t*>(bias0);
     a.bias[1] = static_cast<const uint16_t*>(bias1);
