@@ -280,6 +280,10 @@ template <bool WAVE, int CH, int RB, int YB, bool ODD>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
     __shared__ float part[4][16];
     constexpr bool kAll = CH == 1, kBoth = CH <= 2;   // every vector, or the residual beside y, loaded up front
+    // The vectors of a later step: all runs' at once where there are registers for them (2048 x 28672: 105 us instead
+    // of 119), otherwise run by run, and where the registers are full nothing is moved ahead of its run.  (With two
+    // runs a thread fewer registers leave room for more rows: 777 x 5001 14.1 us run by run, 16.8 at once.)
+    constexpr bool kTogether = CH == 4 && !ODD, kFenced = CH > 2 && !kTogether;
     const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
     const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
     if (WAVE && row >= a.rows) return;   // no barrier follows with WAVE
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
 
     Raw<RB, 8> rr[CH];
     Raw<YB, 8> yr[CH], gr[CH];
-    Affine<8> post, pre;
+    Affine<8> post[kTogether ? CH : 1], pre[kTogether ? CH : 1];
     Raw<RB, 1> rr1;
     Raw<YB, 1> yr1, gr1;
     Affine<1> post1, pre1;
@@ -313,8 +317,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
             for (int c = 0; c < CH; ++c) gr[c].load(a.gate, grow + my.from(c));
         }
         if (kAll) {
-            post.load(a.post_weight, a.post_bias, a.w_type, my.from(0));
-            pre.load(a.weight, a.bias, a.w_type, my.from(0));
+            post[0].load(a.post_weight, a.post_bias, a.w_type, my.from(0));
+            pre[0].load(a.weight, a.bias, a.w_type, my.from(0));
         }
     }
     if (ODD) {
@@ -333,17 +337,29 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
         if (a.flags & SGEMV_NORM_POST) {
             r.clear_outside(my);
             normalize<WAVE, CH, ODD>(r, my, a, part, 0);
+            if (kTogether) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) post[c].load(a.post_weight, a.post_bias, a.w_type, my.from(c));
+            }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                if (!kBoth) asm volatile("" ::: "memory");   // one run's loads at a time: the registers are full
-                if (!kAll) post.load(a.post_weight, a.post_bias, a.w_type, my.from(c));
-                post.apply(r.v[c], a.post_weight, a.post_bias, a);
+                if (kFenced) asm volatile("" ::: "memory");
+                if (!kAll && !kTogether) post[0].load(a.post_weight, a.post_bias, a.w_type, my.from(c));
+                post[kTogether ? c : 0].apply(r.v[c], a.post_weight, a.post_bias, a);
             }
             if (ODD) post1.apply(r.odd, a.post_weight, a.post_bias, a);
         }
+        if (kTogether) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) rr[c].load(a.residual, rrow + my.from(c));
+            if (a.gate) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) gr[c].load(a.gate, grow + my.from(c));
+            }
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            if (!kBoth) {
+            if (kFenced) {
                 asm volatile("" ::: "memory");
                 rr[c].load(a.residual, rrow + my.from(c));
                 if (a.gate) gr[c].load(a.gate, grow + my.from(c));
@@ -380,12 +396,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm(sgemv_norm a) {
     }
     r.clear_outside(my);
     normalize<WAVE, CH, ODD>(r, my, a, part, 2);
+    if (kTogether) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) pre[c].load(a.weight, a.bias, a.w_type, my.from(c));
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         if (my.in(c)) {
-            if (!kBoth) asm volatile("" ::: "memory");
-            if (!kAll) pre.load(a.weight, a.bias, a.w_type, my.at(c));
-            pre.apply(r.v[c], a.weight, a.bias, a);
+            if (kFenced) asm volatile("" ::: "memory");
+            if (!kAll && !kTogether) pre[0].load(a.weight, a.bias, a.w_type, my.at(c));
+            pre[kTogether ? c : 0].apply(r.v[c], a.weight, a.bias, a);
             store(a.x, a.x_type, xrow + my.at(c), r.v[c]);
         }
     }
@@ -468,7 +488,7 @@ extern "C" int sgemv_block_norm(const sgemv_norm* args, void* stream) {
         // Runs a thread.  One is fastest for a few rows, where only latency counts (16 x 5001: 4.8 us, 5.7 with two;
         // 16 x 14336, too long for one: 5.7 with two, 7.4 with four); many long rows want several runs in flight a
         // thread and room for more rows on a compute unit (8192 x 8192: 104 us with two runs, 112 with one, 115 with
-        // four; 512 x 14336: 14.4 us with four, 16.8 with two).
+        // four; 512 x 14336: 13.2 us with four, 16.8 with two).
         int CH = 1;
         if (runs > 1024 || (runs > 512 && a.rows > 256) || (runs > 256 && a.rows > 512)) CH = 2;
         if (runs > 2048 || (runs > 1024 && a.rows > 256)) CH = 4;
