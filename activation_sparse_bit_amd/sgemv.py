@@ -482,6 +482,13 @@ def _row_stride(t, what: str, M: int, n: int) -> int:
     raise ValueError(f"{what}: shape {tuple(shape)}, expected [{M}][>= {n}]")
 
 
+def _fits_int32(what: str, **sizes):
+    """Refuse sizes that the C call's int32 arguments would cut off."""
+    for name, v in sizes.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise SgemvError(SGEMV_ESIZE, f"{what}: {name} = {v}")
+
+
 def _vector(t, what: str, n: int, code: int) -> int:
     """Address of an optional contiguous vector of at least n elements."""
     if t is None:
@@ -556,6 +563,7 @@ def _q4_part(part, group: int, what: str):
     z = None if z is None else _host_codes(z, f"{what} zeros", np.uint8)
     if q.ndim != 2:
         raise ValueError(f"{what} codes: shape {q.shape}, expected [N][K]")
+    _fits_int32(what, N=q.shape[0], K=q.shape[1], group=group)
     want = (q.shape[0], -(-q.shape[1] // group)) if group > 0 else None
     for name, a in (("scales", s), ("zeros", z)):
         if a is not None and want is not None and a.shape != want:
@@ -615,6 +623,7 @@ def sgemv_q4_pack_device(q, scales, zeros=None, up=None, group: int = SGEMV_GROU
     _type_code(scales, "scales")
     torch, parts = _torch, [(q, scales, zeros)] + ([] if up is None else [tuple(up)])
     N, K = q.shape if q.dim() == 2 else (0, 0)
+    _fits_int32("sgemv_q4_pack_device", N=N, K=K, group=group)
     flags = (SGEMV_Q4_ZEROS if zeros is not None else 0) | (SGEMV_Q4_GATED if up is not None else 0) | \
         (SGEMV_Q4_BF16_SCALES if scales.dtype == torch.bfloat16 else 0)
     d, fn = Q4Desc(), lib().sgemv_q4_pack if up is None else lib().sgemv_q4_pack_gated
@@ -656,6 +665,7 @@ def _q4_operands(desc, packed, x, y):
         xt, yt = _TYPES[x.dtype], _TYPES[y.dtype]
         (M, k), (ldx, ex), (rows, n), (ldy, ey) = x.shape, x.stride(), y.shape, y.stride()
         if (rows == M >= 1 and ex == 1 == ey and ldx >= k >= desc.K and ldy >= n >= desc.N and xt < SGEMV_F32
+                and ldx | ldy | M < 1 << 31
                 and (yt == xt or yt == SGEMV_F32) and packed.dtype is _torch.uint8 and packed.is_contiguous()
                 and packed.numel() >= desc.total_bytes):
             return xt, M, ldx, yt, ldy
@@ -672,7 +682,9 @@ def _q4_operands(desc, packed, x, y):
             raise ValueError("packed: expected a torch tensor, got int")
         _require(packed, "packed", _u8(), int(desc.total_bytes))
     M = 1 if x.dim() == 1 else x.shape[0]
-    return xt, M, _row_stride(x, "x", M, desc.K), yt, _row_stride(y, "y", M, desc.N)
+    ldx, ldy = _row_stride(x, "x", M, desc.K), _row_stride(y, "y", M, desc.N)
+    _fits_int32("sgemv_q4_run", rows=M, ldx=ldx, ldy=ldy)
+    return xt, M, ldx, yt, ldy
 
 
 def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
@@ -715,6 +727,7 @@ def _norm_operands(x, residual, y, residual_out, weight, bias, post_weight, post
     rt, xt = _type_code(residual, "residual"), _type_code(x, "x")
     rows = 1 if residual.dim() == 1 else residual.shape[0]
     D = residual.shape[-1] if residual.dim() else 0
+    _fits_int32("sgemv_block_norm", D=D)
     ldr, ldx = _row_stride(residual, "residual", rows, D), _row_stride(x, "x", rows, D)
     device = residual.device
     yt, ldy, yp, ldg, gp, ldo, op = rt, 0, 0, 0, 0, 0, 0
@@ -729,7 +742,7 @@ def _norm_operands(x, residual, y, residual_out, weight, bias, post_weight, post
             raise ValueError("gate: needs y, and y's type")
         if gate.dim() == 1:
             gp = _vector(gate, "gate", D, yt)
-        elif gate.shape[0] == rows and gate.stride(0) == 0:   # one vector, expanded
+        elif gate.dim() == 2 and gate.shape[0] == rows >= 1 and gate.stride(0) == 0:   # one vector, expanded
             gp = _vector(gate[0], "gate", D, yt)
         else:
             ldg, gp = _row_stride(gate, "gate", rows, D), gate.data_ptr()
@@ -758,7 +771,8 @@ def _norm_operands_quick(x, residual, y, residual_out, vectors, gate):
     rt, xt = _TYPES[residual.dtype], _TYPES[x.dtype]
     (rows, D), (ldr, e), device = residual.shape, residual.stride(), residual.device
     (r, n), (ldx, ex) = x.shape, x.stride()
-    if not (e == 1 == ex and r == rows and ldr >= D and ldx >= n >= D and x.device == device and device.type == "cuda"):
+    if not (e == 1 == ex and r == rows and ldr >= D < 1 << 31 and ldx >= n >= D and x.device == device
+            and device.type == "cuda"):
         return None
     yt, ldy, yp, gp, ldg, ldo, op, wt, wp = rt, 0, 0, 0, 0, 0, 0, xt, []
     if y is not None:

@@ -303,3 +303,37 @@ def test_norm_binding_checks():
                      ("shape", lambda: f(x, r, weight=r[0, :49])), ("gate", lambda: f(x, r, r, gate=x))):
         with pytest.raises(ValueError, match=match):
             g()
+
+
+def test_binding_refuses_sizes_beyond_int32():
+    """The C calls take rows, row strides and sizes as int32: larger ones are
+    refused, not cut off (2^32 + 16 would arrive as 16)."""
+    torch = pytest.importorskip("torch")
+    q, s, z = problem(11, 16, 32, 32)
+    desc, blob = sgemv.sgemv_q4_pack(q, s, z, 32)
+    packed = torch.from_numpy(blob)
+    big = 1 << 32
+
+    def meta(rows, n, ld, dtype=torch.float16):
+        return torch.empty_strided((rows, n), (ld, 1), dtype=dtype, device="meta")
+    x, y = meta(2, 32, 32), meta(2, 16, 16)
+    for f in (lambda: sgemv.sgemv_q4_run(desc, packed, meta(2, 32, big + 32), y),
+              lambda: sgemv.sgemv_q4_run(desc, packed, x, meta(2, 16, big + 16)),
+              lambda: sgemv.sgemv_q4_run(desc, packed, x, meta(2, 16, 1 << 31)),
+              lambda: sgemv.sgemv_q4_run(desc, packed, meta(big + 1, 32, 32), meta(big + 1, 16, 16)),
+              lambda: sgemv.sgemv_q4_pack(q, s, z, big + 32),
+              lambda: sgemv.sgemv_q4_pack_device(meta(big + 16, 32, 32, torch.uint8), meta(big + 16, 1, 1)),
+              lambda: sgemv.sgemv_block_norm(meta(1, big + 8, big + 8), meta(1, big + 8, big + 8))):
+        with pytest.raises(sgemv.SgemvError) as e:
+            f()
+        assert e.value.status == sgemv.SGEMV_ESIZE
+
+
+def test_norm_binding_refuses_a_gate_without_dimensions():
+    torch = pytest.importorskip("torch")
+    r = torch.zeros(3, 50)
+    with pytest.raises(ValueError, match="gate"):
+        sgemv.sgemv_block_norm(r, r, r, gate=torch.tensor(1.0))
+    none = torch.zeros(0, 50)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        sgemv.sgemv_block_norm(none, none, none, gate=torch.zeros(60).expand(0, 60))
