@@ -575,13 +575,32 @@ def _is_bf16(s) -> bool:
     return "bfloat16" in str(getattr(s, "dtype", ""))
 
 
+def _bf16_scales(said: bool | None, **scales) -> bool:
+    """Whether the scales (of one matrix or of a pair, by name) are bf16: by
+    their own type, or for uint16 bits as `said` (None: fp16).  Types that
+    contradict `said` or each other are refused, never reinterpreted."""
+    own = {what: _is_bf16(s) for what, s in scales.items()
+           if str(getattr(s, "dtype", "")).endswith("float16")}   # float16 and bfloat16
+    if len(set(own.values())) > 1:
+        raise ValueError("gate and up scales must have one type")
+    for what, bf16 in own.items():
+        if said is not None and bf16 != bool(said):
+            raise ValueError(f"{what} scales are {'bfloat16' if bf16 else 'float16'}, bf16_scales = {said}")
+    if said is not None:
+        return bool(said)
+    if 0 < len(own) < len(scales) and any(own.values()):   # bits beside bf16 scales
+        raise ValueError("gate and up scales must have one type")
+    return any(own.values())
+
+
 def sgemv_q4_pack(q, scales, zeros=None, group: int = SGEMV_GROUP, bf16_scales: bool | None = None):
     """Lay int4 codes q (uint8 [N][K]) with scales [N][ceil(K/group)] (float16,
     bfloat16 or their bits as uint16) and zero-points uint8 (None: symmetric,
     every zero-point 8) out for sgemv_q4_run.  bf16_scales says what uint16
-    scales hold (by default it follows their type).  NumPy arrays or torch
-    tensors.  Returns (Q4Desc, uint8 blob)."""
-    bf16 = _is_bf16(scales) if bf16_scales is None else bf16_scales
+    scales hold (None: fp16); it is refused where scales of a type of their
+    own contradict it.  NumPy arrays or torch tensors.  Returns (Q4Desc, uint8
+    blob)."""
+    bf16 = _bf16_scales(bf16_scales, weight=scales)
     q, s, z = _q4_part((q, scales, zeros), group, "weight")
     flags = (SGEMV_Q4_ZEROS if z is not None else 0) | (SGEMV_Q4_BF16_SCALES if bf16 else 0)
     d = Q4Desc()
@@ -596,10 +615,7 @@ def sgemv_q4_pack(q, scales, zeros=None, group: int = SGEMV_GROUP, bf16_scales: 
 def sgemv_q4_pack_gated(gate, up, group: int = SGEMV_GROUP, bf16_scales: bool | None = None):
     """The same for a gate and an up projection, each (q, scales, zeros) of
     one shape and format, for sgemv_q4_run_gated."""
-    kinds = {_is_bf16(gate[1]), _is_bf16(up[1])}
-    if bf16_scales is None and len(kinds) > 1:
-        raise ValueError("gate and up scales must have one type")
-    bf16 = kinds.pop() if bf16_scales is None else bf16_scales
+    bf16 = _bf16_scales(bf16_scales, gate=gate[1], up=up[1])
     qg, sg, zg = _q4_part(gate, group, "gate")
     qu, su, zu = _q4_part(up, group, "up")
     if qg.shape != qu.shape or (zg is None) != (zu is None):

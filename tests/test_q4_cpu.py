@@ -337,3 +337,30 @@ def test_norm_binding_refuses_a_gate_without_dimensions():
     none = torch.zeros(0, 50)
     with pytest.raises(ValueError, match="GPU tensor"):
         sgemv.sgemv_block_norm(none, none, none, gate=torch.zeros(60).expand(0, 60))
+
+
+def test_packers_refuse_a_scale_type_that_the_scales_contradict():
+    """bf16_scales says what uint16 scales hold; scales that carry a type of
+    their own are never read as another, in either projection of a pair."""
+    torch = pytest.importorskip("torch")
+    q, s, z = problem(12, 17, 130, 64)
+    h, b = torch.from_numpy(s), torch.from_numpy(s.astype(np.float32)).bfloat16()
+    raw = bits(s)
+    for scales, said in ((s, True), (h, True), (b, False)):
+        with pytest.raises(ValueError, match="scales"):
+            sgemv.sgemv_q4_pack(q, scales, z, 64, bf16_scales=said)
+        with pytest.raises(ValueError, match="scales"):
+            sgemv.Q4Matrix(q, scales, z, group=64, device="cpu", bf16_scales=said)
+        for pair in (((q, scales, z), (q, raw, z)), ((q, raw, z), (q, scales, z))):
+            with pytest.raises(ValueError, match="scales"):
+                sgemv.sgemv_q4_pack_gated(*pair, 64, bf16_scales=said)
+    for said in (None, False, True):
+        with pytest.raises(ValueError, match="scales"):
+            sgemv.sgemv_q4_pack_gated((q, b, z), (q, h, z), 64, bf16_scales=said)
+    # what agrees is taken: a type said twice, bits beside a typed projection when it is said what they hold
+    for scales, said in ((s, False), (h, False), (b, True)):
+        want = sgemv.sgemv_q4_pack(q, scales, z, 64)
+        got = sgemv.sgemv_q4_pack(q, scales, z, 64, bf16_scales=said)
+        assert got[0].as_dict() == want[0].as_dict() and np.array_equal(got[1], want[1])
+    got = sgemv.sgemv_q4_pack_gated((q, s, z), (q, raw, z), 64, bf16_scales=False)
+    assert np.array_equal(got[1], sgemv.sgemv_q4_pack_gated((q, s, z), (q, s, z), 64)[1])
