@@ -442,19 +442,22 @@ _device_now = None    # -> index of the current device
 def _load_torch():
     global _torch, _raw_stream, _device_now
     import torch
-    _TYPES.update({torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
     _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
+    # last: a thread that finds its type here uses the others without a check
+    _TYPES.update({torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32})
 
 
 def _type_code(t, what: str) -> int:
     try:
         return _TYPES[t.dtype]
     except (KeyError, AttributeError):
-        if _torch is None:
+        if not _TYPES:
             _load_torch()
-            return _type_code(t, what)
+        code = _TYPES.get(getattr(t, "dtype", None))   # again: another thread may have filled the table meanwhile
+        if code is not None:
+            return code
     if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected float16, bfloat16, float32")

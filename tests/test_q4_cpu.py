@@ -364,3 +364,47 @@ def test_packers_refuse_a_scale_type_that_the_scales_contradict():
         assert got[0].as_dict() == want[0].as_dict() and np.array_equal(got[1], want[1])
     got = sgemv.sgemv_q4_pack_gated((q, s, z), (q, raw, z), 64, bf16_scales=False)
     assert np.array_equal(got[1], sgemv.sgemv_q4_pack_gated((q, s, z), (q, s, z), 64)[1])
+
+
+@pytest.mark.parametrize("when", ["before", "after"])
+def test_first_calls_from_two_threads(monkeypatch, when):
+    """The binding's tables are filled on the first call.  Calls that come
+    from another thread while that happens are answered like any other: here
+    they are made just before and just after the type table is filled."""
+    torch = pytest.importorskip("torch")
+    import threading
+    q, s, z = problem(13, 16, 32, 32)
+    desc, blob = sgemv.sgemv_q4_pack(q, s, z, 32)
+    packed, x, y = torch.from_numpy(blob), torch.zeros(2, 32).half(), torch.zeros(2, 16).half()
+    started, other = [], []
+
+    def second():
+        for call in (lambda: sgemv.sgemv_q4_run(desc, packed, x, y), lambda: sgemv.sgemv_block_norm(x, x)):
+            try:
+                call()
+            except Exception as e:   # noqa: BLE001
+                other.append(e)
+
+    def from_another_thread():
+        if not started:
+            started.append(True)
+            t = threading.Thread(target=second)
+            t.start()
+            t.join()
+
+    class Table(dict):
+        def update(self, *a, **kw):
+            if when == "before":
+                from_another_thread()
+            super().update(*a, **kw)
+            if when == "after":
+                from_another_thread()
+
+    monkeypatch.setattr(sgemv, "_TYPES", Table())
+    for name in ("_torch", "_raw_stream", "_device_now"):
+        monkeypatch.setattr(sgemv, name, None)
+    sgemv._load_torch()
+    assert len(other) == 2
+    for e in other:   # host tensors: both calls are valid up to that check
+        assert type(e) is ValueError and "GPU tensor" in str(e), repr(e)
+    assert sgemv._raw_stream is not None and sgemv._device_now is not None
