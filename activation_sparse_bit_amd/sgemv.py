@@ -678,8 +678,8 @@ def sgemv_q4_desc_from_header(blob) -> Q4Desc:
     return d
 
 
-def _q4_operands(desc, packed, x, y):
-    """Checked (x type, rows, ldx, y type, ldy) of a q4 call."""
+def _q4_operands(desc, packed, x, y, call, out):
+    """Checked (x type, rows, ldx, y type, ldy) of `call`, whose output is named `out`."""
     try:   # what nearly every call brings: two-dimensional operands, checked in few steps
         xt, yt = _TYPES[x.dtype], _TYPES[y.dtype]
         (M, k), (ldx, ex), (rows, n), (ldy, ey) = x.shape, x.stride(), y.shape, y.stride()
@@ -690,19 +690,19 @@ def _q4_operands(desc, packed, x, y):
             return xt, M, ldx, yt, ldy
     except (AttributeError, KeyError, TypeError, ValueError):
         pass
-    xt, yt = _type_code(x, "x"), _type_code(y, "y")
+    xt, yt = _type_code(x, "x"), _type_code(y, out)
     if xt == SGEMV_F32:
         raise ValueError("x: dtype float32, expected float16, bfloat16")
     if yt != xt and yt != SGEMV_F32:
-        raise ValueError(f"y: dtype {str(y.dtype).replace('torch.', '')}, expected x's or float32")
+        raise ValueError(f"{out}: dtype {str(y.dtype).replace('torch.', '')}, expected x's or float32")
     if not (type(packed) is _torch.Tensor and packed.dtype is _torch.uint8 and packed.is_contiguous()
             and packed.numel() >= desc.total_bytes):
         if isinstance(packed, int):
             raise ValueError("packed: expected a torch tensor, got int")
         _require(packed, "packed", _u8(), int(desc.total_bytes))
     M = 1 if x.dim() == 1 else x.shape[0]
-    ldx, ldy = _row_stride(x, "x", M, desc.K), _row_stride(y, "y", M, desc.N)
-    _fits_int32("sgemv_q4_run", rows=M, ldx=ldx, ldy=ldy)
+    ldx, ldy = _row_stride(x, "x", M, desc.K), _row_stride(y, out, M, desc.N)
+    _fits_int32(call, rows=M, ldx=ldx, **{"ld" + out: ldy})
     return xt, M, ldx, yt, ldy
 
 
@@ -711,7 +711,7 @@ def sgemv_q4_run(desc: Q4Desc, packed, x, y, bias=None, stream=None):
     or [M][>= K] with M <= 16, float16 or bfloat16; y is [N] or [M][>= N], of
     x's type or float32; bias is [N] of x's type.  Runs on `stream`, or on the
     current stream of the tensors' device."""
-    xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y)
+    xt, M, ldx, yt, ldy = _q4_operands(desc, packed, x, y, "sgemv_q4_run", "y")
     b = None if bias is None else _vector(bias, "bias", desc.N, xt)
     device = x.device
     _on_one_gpu(device, ("packed", "x", "y", "bias"), (packed, x, y, bias))
@@ -728,7 +728,7 @@ def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=
     "relu".  Operands as for sgemv_q4_run."""
     if act not in _ACTS:
         raise ValueError(f"act: {act!r}, expected one of {', '.join(_ACTS)}")
-    xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h)
+    xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h, "sgemv_q4_run_gated", "h")
     bg = None if bias_gate is None else _vector(bias_gate, "bias_gate", desc.N, xt)
     bu = None if bias_up is None else _vector(bias_up, "bias_up", desc.N, xt)
     device = x.device

@@ -408,3 +408,20 @@ def test_first_calls_from_two_threads(monkeypatch, when):
     for e in other:   # host tensors: both calls are valid up to that check
         assert type(e) is ValueError and "GPU tensor" in str(e), repr(e)
     assert sgemv._raw_stream is not None and sgemv._device_now is not None
+
+
+def test_gated_refusals_name_the_gated_call_and_its_output():
+    torch = pytest.importorskip("torch")
+    part = problem(14, 16, 32, 32)
+    desc, blob = sgemv.sgemv_q4_pack_gated(part, part, 32)
+    packed = torch.from_numpy(blob)
+    far = torch.empty_strided((2, 32), ((1 << 32) + 32, 1), dtype=torch.float16, device="meta")
+    with pytest.raises(sgemv.SgemvError, match="sgemv_q4_run_gated: ldx"):
+        sgemv.sgemv_q4_run_gated(desc, packed, far, torch.zeros(2, 16).half())
+    x = torch.zeros(2, 32).half()
+    for h in (torch.zeros(2, 15).half(), torch.zeros(3, 16).half(), torch.zeros(2, 16).double(), torch.zeros(2, 16).bfloat16(),
+              torch.zeros(16, 2).half().t()):
+        with pytest.raises(ValueError, match="^h: "):
+            sgemv.sgemv_q4_run_gated(desc, packed, x, h)
+        with pytest.raises(ValueError, match="^y: "):
+            sgemv.sgemv_q4_run(desc, packed, x, h)
