@@ -542,6 +542,13 @@ extern "C" int sgemv_q4_pack_device(const uint8_t* q, const uint16_t* scales, co
     if (!packed) return SGEMV_EINVAL;
     if (capacity < a.d.total_bytes) return SGEMV_ESIZE;
     if (!aligned_to(packed, 256) || !aligned_to(scales, 2) || !aligned_to(scales_up, 2)) return SGEMV_EALIGN;
+    const int64_t codes = (int64_t)N * K, groups = (int64_t)N * ((K + group - 1) / group);
+    const SgemvRows out{packed, 1, 0, (int64_t)a.d.total_bytes};
+    const SgemvRows in[6] = {{q, 1, 0, codes}, {scales, 1, 0, 2 * groups}, {with_zeros ? zeros : nullptr, 1, 0, groups},
+                             {gated ? q_up : nullptr, 1, 0, codes}, {gated ? scales_up : nullptr, 1, 0, 2 * groups},
+                             {gated && with_zeros ? zeros_up : nullptr, 1, 0, groups}};
+    for (const SgemvRows& i : in)
+        if (sgemv_overlap(out, i)) return SGEMV_EINVAL;
     a.q[0] = q;
     a.q[1] = q_up;
     a.s[0] = scales;

@@ -478,7 +478,8 @@ int sgemv_q4_pack_gated(const uint8_t* q_gate, const uint16_t* scales_gate,
  *   packed   device buffer of `capacity` bytes, 256-byte aligned (a size query
  *            is sgemv_q4_pack or sgemv_q4_pack_gated with out == NULL)
  * Shapes and types as above, in device memory.  Codes and zero-points are not
- * checked: their low four bits are taken.  EINVAL, ESIZE and EALIGN as above.
+ * checked: their low four bits are taken.  EINVAL, ESIZE and EALIGN as above;
+ * EINVAL also where an input shares bytes with the blob.
  */
 int sgemv_q4_pack_device(const uint8_t* q, const uint16_t* scales, const uint8_t* zeros,
                          const uint8_t* q_up, const uint16_t* scales_up,

@@ -425,3 +425,27 @@ def test_gated_refusals_name_the_gated_call_and_its_output():
             sgemv.sgemv_q4_run_gated(desc, packed, x, h)
         with pytest.raises(ValueError, match="^y: "):
             sgemv.sgemv_q4_run(desc, packed, x, h)
+
+
+def test_device_packer_refuses_inputs_inside_the_blob():
+    """The blob is written while the inputs are read: an input that shares
+    bytes with it is refused."""
+    L = sgemv.lib()
+    d, total = E.Q4Desc(), {}
+    for flags in (2, 3):
+        fn, n = (L.sgemv_q4_pack_gated, 6) if flags & 1 else (L.sgemv_q4_pack, 3)
+        assert fn(*[None] * n, 16, 128, 64, flags, None, 0, d) == E.SGEMV_OK
+        total[flags] = int(d.total_bytes)
+    out, far = FAKE, [FAKE << k for k in range(1, 7)]
+    size = {"q": 16 * 128, "s": 16 * 2 * 2, "z": 16 * 2}
+
+    def pack(flags, **at):
+        p = [at.get(k, far[i]) for i, k in enumerate(("q", "s", "z", "qu", "su", "zu"))]
+        if not flags & 1:
+            p[3:] = [None] * 3
+        return L.sgemv_q4_pack_device(*p, 16, 128, 64, flags, out, 1 << 20, None, None)
+
+    for flags, names in ((2, "q s z"), (3, "q s z qu su zu")):
+        for name in names.split():
+            for at in (out, out + 64, out + total[flags] - 2, out - size[name[0]] + 2):
+                assert pack(flags, **{name: at}) == E.SGEMV_EINVAL, (flags, name, at - out)
