@@ -10,7 +10,7 @@ import math
 
 import numpy as np
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def q4_dequantize(q, s, z, group):
@@ -45,7 +45,7 @@ def gate_function(v, act):
         with np.errstate(over="ignore"):
             return v / (1.0 + np.exp(-v))
     if act == "gelu":
-        return 0.5 * v * (1.0 + _erf(v / math.sqrt(2.0)))
+        return 0.5 * v * _erfc(-v / math.sqrt(2.0))   # 1 + erf(t), which cancels in 64 bits too
     return np.where(v < 0, 0.0, v)
 
 

@@ -402,3 +402,35 @@ def test_offsets_beyond_32_bits():
         s = torch.full((1, -(-K // group)), 0.01, dtype=torch.float16)
         ref = oracle.q4_product(f64(x), q, f64(s), None, group)
         check(y[:, n:n + 1], ref, accumulation(x, (q, s, None), group) + rounding(ref, "f32"), f"row {n}")
+
+
+# ---------------------------------------------------------------------------
+# gates far out, infinities, sums near the end of fp32
+# ---------------------------------------------------------------------------
+def gates_at(values, ups, act):
+    """h in fp32 for gates of exactly -7 .. 7 times `values` (a row each) and
+    up projections of exactly `ups`: one code and one input each."""
+    from activation_sparse_bit_amd import sgemv
+    N, K = 15, 64
+    gate, up = (np.full((N, K), 8, dtype=np.uint8) for _ in range(2))
+    gate[:, 0], up[:, 1] = np.arange(1, 16), 9
+    one = np.ones((N, 1), dtype=np.float16)
+    m = sgemv.Q4Matrix.gated((gate, one, None), (up, one, None), device="cuda:0")
+    x = torch.zeros(len(values), K, dtype=torch.float16)
+    x[:, 0], x[:, 1] = torch.tensor(values), torch.tensor(ups)
+    h = torch.empty(len(values), N, dtype=torch.float32, device="cuda:0")
+    sgemv.sgemv_q4_run_gated(m.desc, m.blob, x.cuda(), h, act=act)
+    return f64(x[:, :1]) * np.arange(-7, 8), f64(x[:, 1:2]), f64(h)
+
+
+def test_gelu_keeps_its_relative_accuracy_far_out():
+    """gelu(v) = v erfc(t) / 2, t = -v / sqrt 2 (relative to the value also
+    where 1 + erf cancels).  t is off by two roundings, 2^-23 of it; erfc's
+    condition number is at most 2 t^2 + 1 = v^2 + 1 (for t < 0 below 1); the
+    library function within 16 steps of 2^-23 (the bound that OpenCL sets),
+    two products 2^-24 each."""
+    import math
+    for values in (np.linspace(0.05, 1.7, 16), np.linspace(0.3, 1.0, 7)):
+        g, u, h = gates_at(values, [1.0 + i / 8 for i in range(len(values))], "gelu")
+        ref = np.vectorize(lambda v: 0.5 * v * math.erfc(-v * math.sqrt(0.5)))(g) * u
+        check(h, ref, np.abs(ref) * (g * g + 1 + 16 + 1) * 2.0 ** -23)

@@ -449,3 +449,9 @@ def test_device_packer_refuses_inputs_inside_the_blob():
         for name in names.split():
             for at in (out, out + 64, out + total[flags] - 2, out - size[name[0]] + 2):
                 assert pack(flags, **{name: at}) == E.SGEMV_EINVAL, (flags, name, at - out)
+
+
+def test_oracle_gelu_far_out():
+    """v Phi(v) with Phi from tables: relative accuracy where 1 + erf cancels."""
+    for v, phi in ((-3.0, 1.3498980316300945e-03), (-6.0, 9.865876450376981e-10), (-10.0, 7.619853024160527e-24)):
+        assert abs(float(oracle.gate_function([v], "gelu")[0]) / (v * phi) - 1) < 1e-12
