@@ -120,7 +120,10 @@ __device__ __forceinline__ bf8_t unpack_bf16(const U& u, uint32_t w) {
 }
 
 __device__ __forceinline__ float gate_of(float v, int act) {
-    if (act == SGEMV_ACT_SILU) return v / (1.0f + expf(-v));
+    if (act == SGEMV_ACT_SILU) {   // v / (1 + e^-v), below zero v e^v / (1 + e^v): e^-v is infinite from -88.7 on
+        const float e = expf(-fabsf(v));
+        return (v < 0.0f ? v * e : v) / (1.0f + e);
+    }
     // erfc(-t) is 1 + erf(t) without its cancellation (at v = -5 the sum has lost 4 % of the value)
     if (act == SGEMV_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
     return v < 0.0f ? 0.0f : v;   // a NaN stays

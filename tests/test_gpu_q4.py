@@ -434,3 +434,16 @@ def test_gelu_keeps_its_relative_accuracy_far_out():
         g, u, h = gates_at(values, [1.0 + i / 8 for i in range(len(values))], "gelu")
         ref = np.vectorize(lambda v: 0.5 * v * math.erfc(-v * math.sqrt(0.5)))(g) * u
         check(h, ref, np.abs(ref) * (g * g + 1 + 16 + 1) * 2.0 ** -23)
+
+
+def test_silu_where_the_exponential_leaves_fp32():
+    """silu(v) = v e^v / (1 + e^v) below zero: e^-v is infinite from v = -88.7
+    on, silu(v) u is not 0 there.  e^v within 3 steps of 2^-23 (OpenCL's
+    bound) and half a subnormal, the sum, the quotient and two products 2^-24
+    each, each at worst half a subnormal (2^-150) more."""
+    g, u, h = gates_at([2.0, 5.0, 11.0, 12.0, 12.25, 12.5, 12.75, 13.0, 13.25, 13.5, 13.75, 14.0, 14.25],
+                       [60000.0] * 11 + [1.0, 512.0], "silu")
+    ref = oracle.gate_function(g, "silu") * u
+    tol = np.abs(ref) * (3 + 2) * 2.0 ** -23 + (np.abs(g) + 2) * np.abs(u) * 2.0 ** -149 + 2.0 ** -149
+    assert (np.abs(ref) > 3 * tol).sum() > 150   # of 195: most are far above the subnormals
+    check(h, ref, tol * (1 + 2.0 ** -20))
