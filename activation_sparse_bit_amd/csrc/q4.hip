@@ -22,6 +22,9 @@
 // are 1024 + q, and (1024 + 16 q) / 16 - 64 for the upper nibbles).  bf16
 // activations: bits 0x4180 | q << 3 are 16 + q, and the group's sum loses
 // (16 + z) * sum x afterwards, sum x being one more matrix product with ones.
+// Where that leaves fp32 (an infinity in x, or 31 times a value), a wavefront
+// goes over its inputs again with exact bf16 integers q - z, for the sums
+// concerned only.
 //
 // A workgroup owns whole outputs: its wavefronts split the inputs, keep
 // their sums in registers, and add them over LDS in wavefront order, so there
@@ -156,6 +159,56 @@ struct Meta {
         return to ? __builtin_amdgcn_alignbit(z, z, (at - to) & 31) : z >> at;
     }
 };
+
+// A wavefront's share of one tile's sums from bf16 activations and the exact
+// integers q - z, for sums that came out of the kernel's own way as no number
+// or an infinity.  Operand row 4 c + i holds row MR c + i of x, so that a lane
+// gets the outputs that it has there.  Rare, so its loop stays rolled: unrolled
+// it would set the kernel's register count (50 -> 85) and with it how many
+// wavefronts hide each other's loads.  8192 x 28672 with 16 rows takes 60 us
+// with an infinity in one row, 125 with a row of NaN, 33 without.
+template <int MR, int P>
+__device__ __forceinline__ float4_t exact_sums(const Q4Args& a, int cell, int wave, int waves) {
+    const int lane = threadIdx.x & 63, n16 = lane & 15, c = lane >> 4;
+    const uint16_t* row = a.x + (int64_t)min((n16 >> 2) * MR + min(n16 & 3, MR - 1), a.M - 1) * a.ldx;
+    float4_t sum = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int step = wave * 4; step < a.blocks * 4; step += (step & 3) == 3 ? waves * 4 - 3 : 1) {
+        const int64_t at = cell + (step >> 2);
+        const int meta = n16 * P + (step & 3) * P / 4;   // the group's place in its cell
+        const uint32_t w = reinterpret_cast<const uint32_t*>(a.w + at * 1024)[lane * 4 + (step & 3)];
+        const uint32_t sb = reinterpret_cast<const uint16_t*>(a.s)[at * (kTileN * P) + meta];
+        const uint32_t zb = a.z_stride ? a.z[at * a.z_stride + (meta >> 1)] >> (4 * (meta & 1)) & 15u : 8u;
+        const float z = (float)zb;
+        const int k0 = step * 32 + 8 * c;
+        uint4_t x = {0, 0, 0, 0}, q;
+        if (k0 + 8 <= a.K) {
+            x = *reinterpret_cast<const uint4_u*>(row + k0);
+        } else {
+#pragma unroll 1
+            for (int k = k0; k < k0 + 8; k += 2) {   // two inputs a turn, moved in from above
+                const uint32_t lo = k < a.K ? row[k] : 0u, hi = k + 1 < a.K ? row[k + 1] : 0u;
+                x = uint4_t{x[1], x[2], x[3], lo | hi << 16};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // small integers: the lower half of their fp32 is zero
+            const float q0 = (float)(w >> (4 * i) & 15u) - z, q1 = (float)(w >> (4 * i + 16) & 15u) - z;
+            q[i] = __builtin_bit_cast(uint32_t, q0) >> 16 | __builtin_bit_cast(uint32_t, q1);
+        }
+        const float4_t zero = {0, 0, 0, 0};
+        const float4_t d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, x), __builtin_bit_cast(bf8_t, q),
+                                                                   zero, 0, 0, 0);
+        const float s = a.s_bf16 ? bf16_f32(sb) : f16_f32(sb);
+#pragma unroll
+        for (int i = 0; i < MR; ++i) {
+            float v = fmaf(s, d[i], sum[i]);
+            asm volatile("" : "+v"(v));   // consumed before the loop's branch, as in the kernel
+            sum[i] = v;
+        }
+    }
+    return sum;
+}
 
 // BF: bf16 activations.  NT: tiles per workgroup (even when gated: a gate
 // tile, then its up tile).  MR: result registers in use: 1, 2, 4 for up to
@@ -311,6 +364,24 @@ __global__ __launch_bounds__(1024) void k_q4(Q4Args a) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < MR; ++i) red[wave * kStride + (t * MR + i) * 64 + lane] = sum[t][i];
+    if constexpr (BF) {
+        bool left = false;   // fp32, for one of this lane's sums
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MR; ++i) left |= !__builtin_isfinite(sum[t][i]);
+        if (__any(left)) {
+#pragma unroll 1
+            for (int t = 0; t < NT; ++t) {
+                const float4_t e = exact_sums<MR, P>(a, min(tile0 + t, a.tiles - 1) * a.blocks, wave, waves);
+#pragma unroll
+                for (int i = 0; i < MR; ++i) {
+                    float& s = red[wave * kStride + (t * MR + i) * 64 + lane];
+                    if (!__builtin_isfinite(s)) s = e[i];
+                }
+            }
+        }
+    }
     __syncthreads();
 
     const int per_wave = NT * MR * 64;

@@ -511,8 +511,9 @@ int sgemv_q4_desc_from_header(const void* header, size_t bytes,
  * fit bf16's mantissa, and CDNA4 has no packed bf16 subtraction) and
  * (z + 16) * sum x is taken off each group's sum in fp32: the accumulation
  * error is relative to sum |s| (q + 16) |x| instead, at most a few 2^-24 of
- * it per group, and a row with an infinity, or with values whose 32-fold sum
- * over a group leaves fp32, gives NaN.
+ * it per group.  Sums that leave fp32 on this way but not by the formula, and
+ * those with an infinity, are computed again from q - z in the same launch, as
+ * fp16 ones are; a call with such a row takes 2 to 5 times as long.
  * EINVAL for NULL, a bad type or description or an overlap; ESIZE for M, ldx
  * or ldy; EALIGN for pointers.
  */

@@ -447,3 +447,58 @@ def test_silu_where_the_exponential_leaves_fp32():
     tol = np.abs(ref) * (3 + 2) * 2.0 ** -23 + (np.abs(g) + 2) * np.abs(u) * 2.0 ** -149 + 2.0 ** -149
     assert (np.abs(ref) > 3 * tol).sum() > 150   # of 195: most are far above the subnormals
     check(h, ref, tol * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("N,K,M,group,zeros", [(48, 260, 6, 64, True), (17, 100, 1, 128, False), (40, 1000, 3, 32, True),
+                                               (8300, 384, 2, 64, True), (8300, 300, 16, 128, True), (8300, 257, 7, 32, False),
+                                               (16500, 300, 16, 32, True), (33000, 384, 12, 64, True), (300, 4224, 16, 64, True),
+                                               (300, 8192, 1, 128, True)])
+def test_bf16_infinities_and_sums_near_the_end_of_fp32(N, K, M, group, zeros):
+    """bf16 rows with an infinity give the infinity or NaN that the formula
+    has, as fp16 rows do; rows of which 32 times the sum leaves fp32, but not
+    the sum itself, give that sum; the other rows keep their bits."""
+    part = problem(N + K, N, K, group, zeros)
+    x = activations(N + M, M, K, "bf16")
+    clean = run_product(x, part, group, "f32")
+    kinds = ["inf", "-inf", "large", "nan", "clean", "two"] if M > 1 else ["inf", "large"]
+    for turn in range(len(kinds) if M == 1 else 1):
+        xs, kind = x.clone(), [kinds[(m + turn) % len(kinds)] for m in range(M)]
+        for m, k in enumerate(kind):
+            at = (K - 1, 7, K // 2)[m % 3]
+            if k in ("inf", "-inf", "nan"):
+                xs[m, at] = float(k)
+            elif k == "large":
+                xs[m, at] = 2e37     # times 31 beyond fp32, times 15 not
+            elif k == "two":
+                xs[m, at], xs[m, at - 3] = float("inf"), float("-inf")
+        got = run_product(xs, part, group, "f32")
+        ref = oracle.q4_product(f64(xs), part[0], f64(part[1]), part[2], group)
+        finite = np.array([k in ("large", "clean") for k in kind])
+        if finite.any():
+            rows = np.flatnonzero(finite)
+            check(got[rows], ref[rows], accumulation(xs[rows], part, group) + rounding(ref[rows], "f32") * 1.01)
+        for m, k in enumerate(kind):
+            if k == "clean":
+                assert torch.equal(got[m], clean[m])
+            elif not finite[m]:
+                assert np.array_equal(f64(got[m]), ref[m], equal_nan=True), (m, k)
+
+
+@pytest.mark.parametrize("N,K,M,group", [(100, 515, 4, 64), (8300, 384, 16, 64), (4200, 300, 2, 128)])
+def test_gated_bf16_infinities(N, K, M, group):
+    from activation_sparse_bit_amd import sgemv
+    gate, up = problem(N, N, K, group), problem(N + 1, N, K, group)
+    m = sgemv.Q4Matrix.gated(gate, up, group=group, device="cuda:0")
+    x = activations(N + 2, M, K, "bf16") * 0.3
+    run = lambda x: sgemv.sgemv_q4_run_gated(m.desc, m.blob, x.cuda(), h, act="relu")  # noqa: E731
+    h = torch.empty(M, N, dtype=torch.float32, device="cuda:0")
+    run(x)
+    clean = h.clone()
+    x[1, K - 1] = float("inf")
+    run(x)
+    rows = [r for r in range(M) if r != 1]
+    assert torch.equal(h[rows], clean[rows])
+    with np.errstate(invalid="ignore"):
+        g, u = (oracle.q4_product(f64(x[1:2]), p[0], f64(p[1]), p[2], group) for p in (gate, up))
+        ref = oracle.gate_function(g, "relu") * u
+    assert np.array_equal(f64(h[1:2]), ref, equal_nan=True)
