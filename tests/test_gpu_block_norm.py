@@ -286,3 +286,48 @@ def test_wide_strides_beyond_32_bits():
     sgemv.sgemv_block_norm(want_x, p["residual"], p["y"], want_r, weight=p["weight"])
     torch.cuda.synchronize()
     assert torch.equal(x, want_x) and torch.equal(rows.contiguous(), want_r)
+
+
+# widths of every number of runs a thread has for few rows (a wavefront a row, 1, 2, 4, 8 runs), with and without odd elements
+WIDTHS = [304, 307, 1000, 4099, 12000, 12003, 20000, 20001, 33000, 33001]
+
+
+@pytest.mark.parametrize("r,y", [(r, y) for r in T for y in T])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_types_at_every_width(D, r, y):
+    """Both norms, a gate a row; x and the vectors take each type in turn."""
+    i = WIDTHS.index(D) + 3 * list(T).index(r) + list(T).index(y)
+    x, w = list(T)[i % 3], list(T)[(i // 3) % 3]
+    check(D + i, 3, D, r, y, x, w, post=True, gate="rows", scale=0.5, center=i % 2 == 0, plus_one=i % 4 == 0, bias=i % 3 == 0)
+
+
+@pytest.mark.parametrize("rows,D", [(300, 8200), (300, 8201), (260, 12003), (257, 16385), (600, 4104), (600, 4097)])
+@pytest.mark.parametrize("r,y", [("f32", "bf16"), ("f32", "f32"), ("f16", "f32"), ("bf16", "bf16")])
+def test_types_of_many_rows(rows, D, r, y):
+    check(rows + D, rows, D, r, y, "bf16", "f32", post=True, gate="rows", scale=0.5, bias=True)
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("r", list(T))
+def test_without_block_output_at_every_width(D, r):
+    """The norm before a model's first block."""
+    check(D, 5, D, r, None, "bf16", "f16", center=D % 3 == 0, r_out=D % 2 == 0)
+
+
+@pytest.mark.parametrize("rows,D", [(3, D) for D in WIDTHS] + [(300, 8200), (300, 8203), (600, 4099), (257, 16400)])
+@pytest.mark.parametrize("gate", [None, "rows"])
+def test_in_place_at_every_width(rows, D, gate):
+    """x in y's place and residual_out in residual's, the two crossed, and x
+    in the gate's place: the bits of the call with buffers of its own."""
+    from activation_sparse_bit_amd import sgemv
+    p = make(rows + D, rows, D, "bf16", "bf16", "bf16", "f32", True, gate, True, False, True)
+    kw = dict(weight=p["weight"], bias=p["bias"], post_weight=p["post_weight"], post_bias=p["post_bias"], scale=0.5, center=True)
+    want_x, want_r = torch.empty_like(p["y"]), torch.empty_like(p["y"])
+    sgemv.sgemv_block_norm(want_x, p["residual"], p["y"], want_r, gate=p["gate"], **kw)
+    for where in ("own", "crossed") + (("gate",) if gate else ()):
+        res, y = p["residual"].clone(), p["y"].clone()
+        g = None if gate is None else p["gate"].clone()
+        x, ro = {"own": (y, res), "crossed": (res, y), "gate": (g, res)}[where]
+        sgemv.sgemv_block_norm(x, res, y, ro, gate=g, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(x, want_x) and torch.equal(ro, want_r), where

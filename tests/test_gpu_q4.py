@@ -502,3 +502,90 @@ def test_gated_bf16_infinities(N, K, M, group):
         g, u = (oracle.q4_product(f64(x[1:2]), p[0], f64(p[1]), p[2], group) for p in (gate, up))
         ref = oracle.gate_function(g, "relu") * u
     assert np.array_equal(f64(h[1:2]), ref, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------
+# kernel instances by size: streamed codes, sixteen wavefronts, pairs of both
+# ---------------------------------------------------------------------------
+def on_gpu(seed, N, K, group, zeros):
+    gen = torch.Generator(device="cuda:0").manual_seed(seed)
+    g = -(-K // group)
+    q = torch.randint(0, 16, (N, K), dtype=torch.uint8, device="cuda:0", generator=gen)
+    s = (0.01 + 0.01 * torch.rand(N, g, device="cuda:0", generator=gen)).half()
+    z = torch.randint(0, 16, (N, g), dtype=torch.uint8, device="cuda:0", generator=gen) if zeros else None
+    return q, s, z
+
+
+def sampled(part, rows):
+    q, s, z = part
+    return q[rows].cpu().numpy(), s[rows].cpu(), None if z is None else z[rows].cpu().numpy()
+
+
+def check_sampled_product(N, K, M, group, xt, zeros=True):
+    from activation_sparse_bit_amd import sgemv
+    part = on_gpu(N + M, N, K, group, zeros)
+    m = sgemv.Q4Matrix(*part, group=group)
+    x = activations(M, M, K, xt)
+    y = torch.full((M + 1, N), float("nan"), dtype=torch.float32, device="cuda:0")
+    sgemv.sgemv_q4_run(m.desc, m.blob, x.cuda(), y[:M])
+    rows = np.array(sorted({0, 1, 15, 16, 33, 63, 64, N // 2, N // 3, N - 17, N - 2, N - 1}))
+    p = sampled(part, rows)
+    ref = oracle.q4_product(f64(x), p[0], f64(p[1]), p[2], group)
+    check(y[:M, rows], ref, accumulation(x, p, group) + rounding(ref, "f32") * 1.01, f"N={N} K={K} M={M}")
+    assert torch.isnan(y[M]).all() and torch.isfinite(y[:M]).all()
+    return m
+
+
+def check_sampled_gated(N, K, M, group, xt, zeros=True):
+    from activation_sparse_bit_amd import sgemv
+    gate, up = on_gpu(N + M, N, K, group, zeros), on_gpu(N + M + 1, N, K, group, zeros)
+    m = sgemv.Q4Matrix.gated(gate, up, group=group)
+    x = activations(M, M, K, xt) * 0.03
+    h = torch.full((M + 1, N), float("nan"), dtype=torch.float32, device="cuda:0")
+    sgemv.sgemv_q4_run_gated(m.desc, m.blob, x.cuda(), h[:M], act="relu")
+    rows = np.array(sorted({0, 1, 15, 16, 31, 33, N // 2, N // 3, N - 17, N - 2, N - 1}))
+    pg, pu = sampled(gate, rows), sampled(up, rows)
+    g, u = (oracle.q4_product(f64(x), p[0], f64(p[1]), p[2], group) for p in (pg, pu))
+    eg, eu = accumulation(x, pg, group), accumulation(x, pu, group)
+    ref = oracle.gate_function(g, "relu") * u   # |relu'| <= 1, one product
+    tol = eg * (np.abs(u) + eu) + np.abs(g) * eu + 2.0 ** -24 * np.abs(ref)
+    check(h[:M, rows], ref, tol * (1 + 2.0 ** -7) + rounding(ref, "f32") * 1.01, f"N={N} K={K} M={M}")
+    assert torch.isnan(h[M]).all() and torch.isfinite(h[:M]).all()
+    return m
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,M", [(8200, 3), (8200, 8), (8200, 15), (20000, 13), (7100, 2), (7100, 16)])
+def test_product_streamed_every_group(N, M, xt, group):
+    K = -(-(96 << 21) // N // 128) * 128 + 37
+    assert check_sampled_product(N, K, M, group, xt, zeros=group != 64).desc.w_bytes >= 96 << 20
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+@pytest.mark.parametrize("N,M", [(4104, 4), (4104, 6), (4104, 16), (10000, 1), (10000, 16)])
+def test_gated_streamed(N, M, xt, group):
+    K = -(-(96 << 20) // N // 128) * 128 + 45
+    assert check_sampled_gated(N, K, M, group, xt, zeros=group != 32).desc.w_bytes >= 96 << 20
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_sixteen_rows_on_sixteen_wavefronts(xt, group):
+    """256 workgroups of one, two and four tiles over long inputs: the most
+    threads and shared memory that a launch has."""
+    check_sampled_product(4096, 4096, 16, group, xt)
+    check_sampled_product(8192, 4096, 16, group, xt)
+    check_sampled_product(16384, 4100, 16, group, xt, zeros=False)
+    check_sampled_gated(4096, 4096, 16, group, xt)
+    check_sampled_gated(8192, 4103, 16, group, xt)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_pairs_and_rows_of_ordinary_size(xt, group):
+    """Pairs of one and two tiles each for few rows, sixteen wavefronts and
+    eight."""
+    for N, K, M in ((1000, 4096, 1), (1000, 4096, 8), (6000, 1000, 4), (6000, 8200, 8), (14336, 520, 2), (9000, 4096, 1)):
+        check_sampled_gated(N, K, M, group, xt, zeros=M != 4)
