@@ -3,12 +3,16 @@
 //   u = y or norm(y),  r = residual + scale * gate * u,  x = norm(r)
 //   norm(v) = (v - c) / sqrt(mean((v - c)^2) + eps) * w + b
 //
-// One workgroup (one wavefront for short rows) owns a row and keeps it in
-// registers as fp32 from the first load to the last store, so every byte
-// moves once and both norms see unrounded values.  Means and squared
-// deviations are two sums over the row each (the deviations are taken from
-// the mean, not from a difference of large sums), added over the lanes of a
-// wavefront and then over the wavefronts in a fixed order.
+// One workgroup (one wavefront for short rows) owns a row and keeps it as fp32
+// from the first load to the last store, so every byte moves once and both
+// norms see unrounded values.  In registers, that is, of which a thread has
+// 128: by the compiler's report four runs a thread of an odd width (from 16392
+// elements on, from 8200 with more than 256 rows) leave 8 bytes a lane in
+// scratch, 200 with an fp32 residual and 16-bit y, and eight runs (from 32776
+// on) 132 to 844.  Means and squared deviations are two sums over the row each
+// (the deviations are taken from the mean, not from a difference of large
+// sums), added over the lanes of a wavefront and then over the wavefronts in a
+// fixed order.
 //
 // A thread owns runs of eight elements, moved as 16-byte pieces at whatever
 // address the row has (pieces off a 16-byte boundary cost 3 to 7 % here), and
@@ -16,9 +20,13 @@
 // of eight leaves over.  No element has two owners, so outputs may take the
 // place of inputs.
 //
-// Many rows are bound by HBM: 16384 x 4096 (bf16, both norms, 537 MB) in 95 to
-// 102 us, 5.3 to 5.6 TB/s, what a copy reaches.  Few rows are latency: 1 x 4096 in
-// 2.5 us, 16 x 8192 with both norms in 5.0, each sum over a row about 0.5 of it.
+// Many rows are bound by HBM: 16384 x 4096 (bf16, both norms, 537 MB) in 94 to
+// 99 us, 5.4 to 5.7 TB/s, with an fp32 residual (805 MB) in 143; a library copy
+// reaches 5.3.  Few rows are latency: 1 x 4096 in 2.5 us, 16 x 8192 with both
+// norms in 5.0, each sum over a row about 0.5 of it.  Odd widths, whose rows are
+// few and long, wait at four sums a row: 777 x 5001 in 14.4 us (2.7 TB/s), 300 x
+// 12003 with an fp32 residual 19.0 (300 x 12000: 13.1), 300 x 20001 33.8 (20000:
+// 20.9).  Above 32768 elements: 300 x 65536 95.8 us, 1.6 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

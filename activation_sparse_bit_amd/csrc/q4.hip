@@ -32,12 +32,15 @@
 // depend on timing.
 //
 // Bound by HBM where the matrix is large: 100003 x 4096 (four rows, 219 MB) in
-// 36 us, 6.0 TB/s, the vector units 80 % busy; 28672 x 8192 gated (16 rows, 251
-// MB) in 52 us.  With sixteen rows the L2 counts too: 8192 x 28672 (123 MB) in
-// 32 us, its activations read 256 times (235 MB).  A small one (2048 x 2048, 3.1
-// us) is launch and latency.  Many resident wavefronts hide the latency, not
-// prefetching: two blocks in flight a wavefront cost registers and gained 3 %
-// at most.
+// 35 to 42 us, 5.2 to 6.2 TB/s, the vector units 66 to 80 % busy; 28672 x 8192
+// gated (16 rows, 251 MB) in 50 to 52 us.  With sixteen rows the L2 counts too:
+// 8192 x 28672 (123 MB) in 32 us, its activations read 256 times (235 MB).  A
+// matrix that stays in the 256 MB cache is read from there, and then its start
+// and end count: 4096 x 14336 takes 7.4 us warm and 10.8 cold, 14336 x 4096
+// gated 12.3 and 14.7.  A small one (2048 x 2048, 2.6 us warm, 4.0 cold) is
+// launch and latency.  Many resident wavefronts hide the latency, not
+// prefetching: two blocks in flight a wavefront cost registers and gained 3 % at
+// most.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -580,9 +583,13 @@ int run(const sgemv_q4_desc* d, const void* packed, const void* x, int x_type, i
     while (waves > 1 && waves > a.blocks) waves /= 2;
     const int P = kBlockK / d->group;
     // A matrix that takes a good part of the 256 MB cache is gone from it before its next use: its codes are read past
-    // the caches (100003 x 4096, 219 MB: 48.7 -> 41.6 us; 28672 x 8192 gated, 16 rows: 58.2 -> 53.2).  Smaller ones may
-    // stay from one token to the next, and reading past the caches would lose that (61 MB, called in turn with two
-    // others of its size: 12.7 -> 15.5 us).
+    // the caches (warm, three matrices in turn: 100003 x 4096 42.0 -> 39.2 us, 28672 x 8192 gated, 16 rows, 56.9 -> 52.2;
+    // cold, more than 600 MB in turn: 44.2 -> 41.4 and 62.2 -> 56.2).  Smaller ones may stay from one token to the next,
+    // and reading past the caches would lose more then than it gains when they are cold: 4096 x 14336 7.4 -> 8.8 us warm,
+    // 10.7 -> 10.2 cold; 8192 x 14336 12.1 -> 13.0 and 14.6 -> 14.0; 14336 x 4096 gated 12.8 -> 13.6 and 14.7 -> 14.3.
+    // Workgroups of one tile read through the caches whatever the size (that many codes in fewer than 512 tiles take
+    // more than 24000 inputs): 7168 x 28672 past the caches 22.1 -> 21.1 us warm, 26.4 -> 25.8 cold, 16 rows 44.2 -> 43.2
+    // and 46.8 -> 42.2, not worth 18 more kernels.
     const bool streamed = d->w_bytes >= (96ull << 20);
     const Kernel k = a.x_bf16 ? pick<true>(NT, MR, P, streamed) : pick<false>(NT, MR, P, streamed);
     return launch(a, k, NT, waves, static_cast<hipStream_t>(stream));

@@ -725,7 +725,8 @@ _ACTS = {"silu": SGEMV_ACT_SILU, "gelu": SGEMV_ACT_GELU, "relu": SGEMV_ACT_RELU}
 def sgemv_q4_run_gated(desc: Q4Desc, packed, x, h, act: str = "silu", bias_gate=None, bias_up=None, stream=None):
     """h = act(gate . x + bias_gate) * (up . x + bias_up) over 4-bit weights
     packed by sgemv_q4_pack_gated; act is "silu", "gelu" (error function) or
-    "relu".  Operands as for sgemv_q4_run."""
+    "relu".  Operands as for sgemv_q4_run.  h goes on to sgemv_q4_run, or, as
+    float16, to sgemv_run_fused."""
     if act not in _ACTS:
         raise ValueError(f"act: {act!r}, expected one of {', '.join(_ACTS)}")
     xt, M, ldx, ht, ldh = _q4_operands(desc, packed, x, h, "sgemv_q4_run_gated", "h")

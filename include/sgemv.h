@@ -526,7 +526,8 @@ int sgemv_q4_run(const sgemv_q4_desc* d, const void* packed, const void* x,
  * launch:
  *   h[m][n] = act(gate[n] . x[m] + bias_gate[n]) * (up[n] . x[m] + bias_up[n])
  * both sums and the gate function in fp32, one rounding to h_type.  h is
- * what the down projection takes, for instance sgemv_run_fused.
+ * what the down projection takes: sgemv_q4_run, or sgemv_run_fused, which
+ * skips the columns of small h and takes fp16 only.
  *
  *   d    host description with SGEMV_Q4_GATED
  *   act  SGEMV_ACT_*
@@ -578,7 +579,8 @@ typedef struct sgemv_norm {
  * factor 1, a NULL bias 0, and SGEMV_NORM_PLUS_ONE adds 1 to weights that
  * are given.  With y == NULL, r = residual (gate and SGEMV_NORM_POST are
  * then refused).  Everything is computed in fp32 and rounded once on the way
- * out; x is the norm of r before its rounding to residual_type.
+ * out; x is the norm of r before its rounding to residual_type.  A row's sum
+ * of squares has to fit fp32 (values below 7 * 10^16 do at any width).
  *
  * Row strides are at least D and pointers need the alignment of their
  * elements only.  An output may be the very buffer of residual, y or a
