@@ -641,7 +641,13 @@ def sgemv_q4_pack_device(q, scales, zeros=None, up=None, group: int = SGEMV_GROU
     checked, which waits for the GPU.  Returns (Q4Desc, uint8 GPU tensor)."""
     _type_code(scales, "scales")
     torch, parts = _torch, [(q, scales, zeros)] + ([] if up is None else [tuple(up)])
-    N, K = q.shape if q.dim() == 2 else (0, 0)
+    for name, part in zip(("weight", "up"), parts):
+        for kind, t in zip(("codes", "scales", "zeros"), part):
+            if not isinstance(t, torch.Tensor) and (kind != "zeros" or t is not None):
+                raise ValueError(f"{name} {kind}: expected a torch tensor, got {type(t).__name__}")
+    if q.dim() != 2:
+        raise ValueError(f"weight codes: shape {tuple(q.shape)}, expected [N][K]")
+    N, K = q.shape
     _fits_int32("sgemv_q4_pack_device", N=N, K=K, group=group)
     flags = (SGEMV_Q4_ZEROS if zeros is not None else 0) | (SGEMV_Q4_GATED if up is not None else 0) | \
         (SGEMV_Q4_BF16_SCALES if scales.dtype == torch.bfloat16 else 0)
@@ -700,7 +706,7 @@ def _q4_operands(desc, packed, x, y, call, out):
         if isinstance(packed, int):
             raise ValueError("packed: expected a torch tensor, got int")
         _require(packed, "packed", _u8(), int(desc.total_bytes))
-    M = 1 if x.dim() == 1 else x.shape[0]
+    M = 1 if x.dim() < 2 else x.shape[0]
     ldx, ldy = _row_stride(x, "x", M, desc.K), _row_stride(y, out, M, desc.N)
     _fits_int32(call, rows=M, ldx=ldx, **{"ld" + out: ldy})
     return xt, M, ldx, yt, ldy
@@ -745,7 +751,7 @@ _NORM = struct.Struct("@qiI9P5q2f4i")
 def _norm_operands(x, residual, y, residual_out, weight, bias, post_weight, post_bias, gate):
     """Checked (rows, D, addresses, strides, types) of a sgemv_block_norm call."""
     rt, xt = _type_code(residual, "residual"), _type_code(x, "x")
-    rows = 1 if residual.dim() == 1 else residual.shape[0]
+    rows = 1 if residual.dim() < 2 else residual.shape[0]
     D = residual.shape[-1] if residual.dim() else 0
     _fits_int32("sgemv_block_norm", D=D)
     ldr, ldx = _row_stride(residual, "residual", rows, D), _row_stride(x, "x", rows, D)

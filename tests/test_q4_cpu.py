@@ -455,3 +455,29 @@ def test_oracle_gelu_far_out():
     """v Phi(v) with Phi from tables: relative accuracy where 1 + erf cancels."""
     for v, phi in ((-3.0, 1.3498980316300945e-03), (-6.0, 9.865876450376981e-10), (-10.0, 7.619853024160527e-24)):
         assert abs(float(oracle.gate_function([v], "gelu")[0]) / (v * phi) - 1) < 1e-12
+
+
+def test_binding_refuses_operands_without_dimensions_and_other_kinds():
+    torch = pytest.importorskip("torch")
+    q, s, z = problem(15, 16, 32, 32)
+    desc, blob = sgemv.sgemv_q4_pack(q, s, z, 32)
+    packed, x, y = torch.from_numpy(blob), torch.zeros(2, 32).half(), torch.zeros(2, 16).half()
+    point, r = torch.tensor(1.0).half(), torch.zeros(3, 50)
+    qt, st, zt = torch.from_numpy(q), torch.from_numpy(s), torch.from_numpy(z)
+    for match, f in (("^x: ", lambda: sgemv.sgemv_q4_run(desc, packed, point, y)),
+                     ("^y: ", lambda: sgemv.sgemv_q4_run(desc, packed, x, point)),
+                     ("^x: ", lambda: sgemv.sgemv_q4_run(desc, packed, None, y)),
+                     ("^bias: ", lambda: sgemv.sgemv_q4_run(desc, packed, x, y, bias=point)),
+                     ("^packed: ", lambda: sgemv.sgemv_q4_run(desc, blob, x, y)),
+                     ("^residual: ", lambda: sgemv.sgemv_block_norm(r, torch.tensor(1.0))),
+                     ("^x: ", lambda: sgemv.sgemv_block_norm(torch.tensor(1.0), r)),
+                     ("^y: ", lambda: sgemv.sgemv_block_norm(r, r, torch.tensor(1.0))),
+                     ("^weight: ", lambda: sgemv.sgemv_block_norm(r, r, weight=torch.tensor(1.0))),
+                     ("^residual_out: ", lambda: sgemv.sgemv_block_norm(r, r, r, torch.tensor(1.0))),
+                     ("^weight codes: ", lambda: sgemv.sgemv_q4_pack_device(q, st, zt, group=32)),
+                     ("^weight codes: ", lambda: sgemv.sgemv_q4_pack_device(qt[0], st, zt, group=32)),
+                     ("^weight zeros: ", lambda: sgemv.sgemv_q4_pack_device(qt, st, z, group=32)),
+                     ("^up codes: ", lambda: sgemv.sgemv_q4_pack_device(qt, st, zt, up=(q, st, zt), group=32)),
+                     ("^up scales: ", lambda: sgemv.sgemv_q4_pack_device(qt, st, zt, up=(qt, s, zt), group=32))):
+        with pytest.raises(ValueError, match=match):
+            f()
