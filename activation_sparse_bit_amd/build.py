@@ -2,8 +2,8 @@
 ``lib/libsgemv_bench.so``) in-tree for gfx950.
 
 The host packers (pack.cpp, pack_q4.cpp) are plain C++ built with g++; the
-kernels and the C ABI (sgemv.hip, q4.hip, norm.hip) are built with hipcc for
-gfx950.  All HIP code is compiled with packed-fp32 instructions disabled.
+kernels and the C ABI (the .hip files) are built with hipcc for gfx950, several
+at a time.  All HIP code is compiled with packed-fp32 instructions disabled.
 """
 from __future__ import annotations
 
@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +20,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsgemv.so")
 BENCH_LIB = os.path.join(LIBDIR, "libsgemv_bench.so")   # measurement-only read kernels
+
+HOST = ("pack", "pack_q4")
+DEVICE = ("sgemv", "q4", "norm", "attn", "rotary", "beam", "pages")
 
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -48,23 +52,20 @@ def build(verbose: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     obj_dir = os.path.join(LIBDIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
-    objs = []
-    for name in ("pack", "pack_q4"):
-        objs.append(os.path.join(obj_dir, name + ".o"))
-        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-c",
-              os.path.join(CSRC, name + ".cpp"), "-o", objs[-1]], verbose)
-    for name in ("sgemv", "q4", "norm"):
-        objs.append(os.path.join(obj_dir, name + ".o"))
-        _run([_hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, name + ".hip"),
-              "-o", objs[-1]], verbose)
+    obj = lambda name: os.path.join(obj_dir, name + ".o")  # noqa: E731
+    jobs = [["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-c",
+             os.path.join(CSRC, name + ".cpp"), "-o", obj(name)] for name in HOST]
+    jobs += [[_hipcc(), *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, name + ".hip"), "-o", obj(name)]
+             for name in DEVICE + ("bench_read",)]
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
+    objs = [obj(name) for name in HOST + DEVICE]
     tmp = LIB + ".tmp"
     _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     # the measurement kernels (memory ceilings), a library of their own
-    bench_o = os.path.join(obj_dir, "bench_read.o")
-    _run([_hipcc(), *HIP_FLAGS, "-c", os.path.join(CSRC, "bench_read.hip"), "-o", bench_o], verbose)
     tmp = BENCH_LIB + ".tmp"
-    _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", bench_o, "-o", tmp], verbose)
+    _run([_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", obj("bench_read"), "-o", tmp], verbose)
     os.replace(tmp, BENCH_LIB)
     return LIB
 

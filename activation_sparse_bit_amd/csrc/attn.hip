@@ -1,0 +1,741 @@
+// Attention of one new token per sequence over a paged cache: sgemv_attn_paged.
+//
+//   z_i = scale q . k_i,   out = sum_i e^(z_i - m) v_i / sum_i e^(z_i - m)
+//
+// One pass over the keys and values with a running maximum m, sum and output.
+// The query heads that share a key head (up to 16, more take several passes)
+// are the columns of v_mfma_f32_16x16x32: keys as the rows give z for 16
+// tokens and 16 heads, values as the rows give 16 output elements for 16
+// heads.  A lane's four scores of each of two products belong to one head and
+// eight tokens, and those eight tokens are just what its slots of the second
+// product's operand want, so probabilities never leave their lane, and the
+// running maximum, its correction and the output belong to the lane's head.
+// Values are read in rows (16 bytes a lane, whole rows by neighbouring lanes);
+// a lane that reads eight tokens' eight elements turns them by byte permutes
+// into eight operands of eight tokens each.
+//
+// Work is split evenly whatever the lengths: all sequences' units of 128
+// tokens, sequence by sequence and head by head, form one line that is cut
+// into equal runs, one for each workgroup.  A run's first and last piece may
+// be part of a head; such pieces go to the workspace, and the last workgroup
+// of that head to arrive joins them in the order of the tokens.  The cut
+// follows from the lengths alone, so results do not depend on timing.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kv.h"
+
+namespace {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2_u __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t uint4_u __attribute__((ext_vector_type(4), aligned(8)));
+
+constexpr int kWaves = 4;
+constexpr int kTile = 32;                 // tokens of a wavefront's step
+constexpr int kUnit = kWaves * kTile;     // tokens of a workgroup's step
+constexpr int kRows = 16;                 // query heads of one key head at a time
+constexpr int kMaxPieces = 128;           // of one head
+constexpr int kMaxHeads = 4096;           // heads (of all sequences) of one launch
+constexpr int kCounterStep = 16;          // words between arrival counters
+constexpr int kGrid = 1024;
+constexpr size_t kCounterBytes = (size_t)kMaxHeads * kCounterStep * 4;
+constexpr uint32_t kCacheSC1 = 16;        // cache policy: coherent at device scope
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct Args {
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t k_page, k_token, k_head, v_page, v_token, v_head;   // bytes
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* lengths;
+    uint32_t* counters;
+    void* partial;
+    int64_t q_row, q_head, out_row, out_head, ld_table;
+    SgemvDiv page;
+    int32_t pages, capacity;      // pages of the cache, tokens that a table's row can list
+    int32_t batch, heads, groups, group, tiles;   // query heads, key heads x tiles, heads a key head, tiles of 16
+    int32_t dim, window;
+    int32_t q_vector;             // whether q can be read in 16 bytes
+    uint32_t partial_bytes, slot_bytes;
+    float scale, softcap;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
+__device__ __forceinline__ uint32_t as_u32(float v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ int divide(int n, const SgemvDiv& d) { return (int)(((uint64_t)(uint32_t)n * d.m) >> d.s); }
+
+// Largest and sum over the four lanes that hold one head (16 and 32 apart).
+__device__ __forceinline__ float head_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = fmaxf(as_float(a[0]), as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return fmaxf(as_float(b[0]), as_float(b[1]));
+}
+__device__ __forceinline__ float head_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = as_float(a[0]) + as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return as_float(b[0]) + as_float(b[1]);
+}
+
+struct F16 {
+    using pair = half2_t;
+    using frag = half8_t;
+    // Probabilities are held 2^15 times their size: fp16 then keeps those down to 2^-29 of the largest exactly as
+    // well as it keeps the largest.
+    static constexpr float kLift = 15.0f;
+    static __device__ __forceinline__ float4_t mfma(frag a, frag b, float4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t two(float a, float b) {
+        return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+    }
+    static __device__ __forceinline__ uint16_t one(float a) { return __builtin_bit_cast(uint16_t, (_Float16)a); }
+    template <bool HIGH>
+    static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
+    }
+};
+
+struct BF16 {
+    using pair = bf2_t;
+    using frag = bf8_t;
+    static constexpr float kLift = 0.0f;
+    static __device__ __forceinline__ float4_t mfma(frag a, frag b, float4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t two(float a, float b) {
+        return __builtin_bit_cast(uint32_t, bf2_t{(__bf16)a, (__bf16)b});
+    }
+    static __device__ __forceinline__ uint16_t one(float a) { return __builtin_bit_cast(uint16_t, (__bf16)a); }
+    template <bool HIGH>
+    static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+    }
+};
+
+// Tokens of a sequence: [lo, len) are seen; units count from `first`.
+struct Span {
+    int len, lo, first, units;
+    bool bad;
+};
+__device__ __forceinline__ Span span_of(int len, const Args& a) {
+    Span s;
+    s.bad = len < 0 || len > a.capacity;
+    s.len = s.bad ? 0 : len;
+    s.lo = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
+    s.first = s.lo & ~(kTile - 1);
+    s.units = (s.len - s.first + kUnit - 1) / kUnit;
+    if (s.units < 1) s.units = 1;   // an empty sequence's output is written too
+    return s;
+}
+
+// PAIRS: 64s of elements that a head's keys are padded to.  VW: value elements
+// of a lane, VB blocks of 16 of them.  WHOLE: page_size is a multiple of 16, so
+// 16 tokens from a multiple of 16 on lie in one page.
+template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE>
+struct Attention {
+    static constexpr int STEPS = 2 * PAIRS;
+    static constexpr int KLOADS = E4M3 ? PAIRS : STEPS;   // 16-byte loads of a token's row by four lanes
+    static constexpr int DPAD = VB * 16 * VW;
+    static constexpr int VBYTES = VW * (E4M3 ? 1 : 2);
+    static constexpr int VWORDS = VBYTES / 4;
+    static constexpr int ES = E4M3 ? 1 : 2;
+    static constexpr int LDO = 16 * VW + 4;               // floats between rows of the exchange
+
+    struct Shared {
+        union {
+            float o[kWaves][kRows][LDO];
+            float2 join[kRows][kMaxPieces];               // weight (first the maximum) and sum of every piece
+        };
+        float m[kWaves][kRows], l[kWaves][kRows];
+        float row_m[kRows], row_l[kRows];
+        int scan[kWaves], most[kWaves], found[2];
+        int last;
+    };
+
+    uint4_t kr[2][KLOADS];
+    uint32_t vr[8][VB][VWORDS];
+    typename T::frag qf[STEPS];
+    float4_t o[VB][VW];
+    float m, l;
+
+    static __device__ __forceinline__ uint4_t load16(const uint8_t* p) {
+        return __builtin_bit_cast(uint4_t, *reinterpret_cast<const uint4_u*>(p));
+    }
+
+    // First element of a lane's eight of step s.
+    static __device__ __forceinline__ int key_dim(int s, int g) {
+        return E4M3 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+    }
+
+    __device__ __forceinline__ void load_q(const Args& a, int b, int head, int g) {
+        const uint16_t* q = a.q + b * a.q_row + head * a.q_head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = key_dim(s, g);
+            uint4_t w = {0, 0, 0, 0};
+            if (d < a.dim) {
+                if (a.q_vector) {
+                    w = *reinterpret_cast<const uint4_t*>(q + d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = q[d + 2 * j] | (uint32_t)q[d + 2 * j + 1] << 16;
+                }
+            }
+            qf[s] = __builtin_bit_cast(typename T::frag, w);
+        }
+    }
+
+    __device__ __forceinline__ void load_key(const Args& a, int which, const uint8_t* row, int g) {
+#pragma unroll
+        for (int s = 0; s < KLOADS; ++s) {
+            const int d = E4M3 ? 64 * s + 16 * g : 32 * s + 8 * g, n = E4M3 ? 16 : 8;
+            const bool inside = E4M3 ? s < PAIRS - 1 : s < STEPS - 2;   // of any head that this kernel serves
+            if (inside || a.dim == PAIRS * 64 || d + n <= a.dim) {
+                kr[which][s] = load16(row + d * ES);
+            } else {   // beyond a head's end: zero, since what stands there may be anything
+                uint4_t w = {0, 0, 0, 0};
+                if (E4M3 && d + 8 <= a.dim) {
+                    const uint2_t half = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(row + d));
+                    w[0] = half[0];
+                    w[1] = half[1];
+                }
+                kr[which][s] = w;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load_value(const Args& a, int j, const uint8_t* row, int c) {
+#pragma unroll
+        for (int nb = 0; nb < VB; ++nb) {
+            const int d = (nb * 16 + c) * VW;
+            const uint8_t* p = row + (d < a.dim ? d : 0) * ES;   // beyond a head's end: rows of the result that nobody reads
+            if constexpr (VWORDS == 4) {
+                const uint4_t w = load16(p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vr[j][nb][i] = w[i];
+            } else if constexpr (VWORDS == 2) {
+                const uint2_t w = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(p));
+                vr[j][nb][0] = w[0];
+                vr[j][nb][1] = w[1];
+            } else {
+                vr[j][nb][0] = *reinterpret_cast<const uint32_t*>(p);
+            }
+        }
+    }
+
+    // One step: 32 tokens from t0 on, some of them in [lo, len).  Returns
+    // whether a page in use does not exist.
+    __device__ __forceinline__ bool step(const Args& a, const Span& span, const int32_t* pages, int64_t k_off,
+                                         int64_t v_off, int t0, float z_scale) {
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+        bool bad = false;
+        if constexpr (WHOLE) {
+            const int ta = t0, tb = t0 + 16 < span.len ? t0 + 16 : t0;
+            const int pa = divide(ta, a.page), pb = divide(tb, a.page);
+            int ia = pages[pa], ib = pages[pb];
+            if ((uint32_t)ia >= (uint32_t)a.pages) { bad = true; ia = 0; }
+            if ((uint32_t)ib >= (uint32_t)a.pages) { bad = true; ib = 0; }
+            const int oa = ta - pa * (int)a.page.d, ob = tb - pb * (int)a.page.d;
+            const uint8_t* ka = a.k + k_off + ia * a.k_page + oa * a.k_token;
+            const uint8_t* kb = a.k + k_off + ib * a.k_page + ob * a.k_token;
+            const uint8_t* va = a.v + v_off + ia * a.v_page + oa * a.v_token;
+            const uint8_t* vb = a.v + v_off + ib * a.v_page + ob * a.v_token;
+            load_key(a, 0, ka + c * a.k_token, g);
+            load_key(a, 1, kb + c * a.k_token, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                load_value(a, j, va + (4 * g + j) * a.v_token, c);
+                load_value(a, 4 + j, vb + (4 * g + j) * a.v_token, c);
+            }
+        } else {
+            const int mine = t0 + (lane & 31) < span.len ? t0 + (lane & 31) : span.len - 1;
+            const int p = divide(mine, a.page);
+            int id = pages[p];
+            const int in = mine - p * (int)a.page.d;
+            if ((uint32_t)id >= (uint32_t)a.pages) { bad = true; id = 0; }
+            bad = __ballot(bad) != 0;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int i = __shfl(id, 16 * w + c), t = __shfl(in, 16 * w + c);
+                load_key(a, w, a.k + k_off + i * a.k_page + t * a.k_token, g);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int from = 16 * (j >> 2) + 4 * g + (j & 3);
+                const int i = __shfl(id, from), t = __shfl(in, from);
+                load_value(a, j, a.v + v_off + i * a.v_page + t * a.v_token, c);
+            }
+        }
+
+        float4_t z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                uint4_t f;
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = kr[w][s >> 1][2 * (s & 1) + i];
+                        f[2 * i] = T::template from_e4m3<false>(x);
+                        f[2 * i + 1] = T::template from_e4m3<true>(x);
+                    }
+                } else {
+                    f = kr[w][s];
+                }
+                z[w] = T::mfma(__builtin_bit_cast(typename T::frag, f), qf[s], z[w]);
+            }
+        // a result has to be read in the block that makes it: a read behind a branch can miss its wait states
+        asm volatile("" : "+v"(z[0]), "+v"(z[1]));
+
+        const bool edge = t0 < span.lo || t0 + kTile > span.len;
+        float t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = z[j >> 2][j & 3] * z_scale;
+        if (a.softcap > 0.0f) {   // in units of log2(e), as without it
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = t[j] * (1.0f / a.softcap);
+                t[j] = a.softcap * kLog2e * tanhf(x);
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tok = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                const bool seen = tok >= span.lo && tok < span.len;
+                if (!seen) {
+                    t[j] = -INFINITY;
+#pragma unroll
+                    for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                        for (int i = 0; i < VWORDS; ++i) vr[j][nb][i] = 0;
+                }
+            }
+        }
+        float top = t[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, t[j]);
+        top = fmaxf(m, head_max(top));
+        const float base = top == -INFINITY ? 0.0f : top;
+        if (__ballot(top != m)) {
+            const float by = __builtin_amdgcn_exp2f(m - base);
+            l *= by;
+#pragma unroll
+            for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                for (int r = 0; r < VW; ++r) o[nb][r] *= by;
+            m = top;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            t[j] = __builtin_amdgcn_exp2f(t[j] - base + T::kLift);
+            sum += t[j];
+        }
+        l += sum;
+        const uint4_t pw = {T::two(t[0], t[1]), T::two(t[2], t[3]), T::two(t[4], t[5]), T::two(t[6], t[7])};
+        const auto pf = __builtin_bit_cast(typename T::frag, pw);
+#pragma unroll
+        for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+            for (int r2 = 0; r2 < VW / 2; ++r2) {   // elements 2 r2 and 2 r2 + 1 of the lane's
+                uint32_t x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (E4M3) {
+                        const uint32_t w = vr[j][nb][r2 >> 1];
+                        x[j] = r2 & 1 ? T::template from_e4m3<true>(w) : T::template from_e4m3<false>(w);
+                    } else {
+                        x[j] = vr[j][nb][r2];
+                    }
+                }
+                uint4_t lo, hi;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lo[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
+                    hi[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
+                }
+                o[nb][2 * r2] = T::mfma(__builtin_bit_cast(typename T::frag, lo), pf, o[nb][2 * r2]);
+                o[nb][2 * r2 + 1] = T::mfma(__builtin_bit_cast(typename T::frag, hi), pf, o[nb][2 * r2 + 1]);
+            }
+#pragma unroll
+        for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+            for (int r = 0; r < VW; ++r) asm volatile("" : "+v"(o[nb][r]));
+        return bad;
+    }
+
+    // Joins the pieces of a head, in the order of their tokens.
+    static __device__ void join(const Args& a, Shared& sh, __amdgpu_buffer_rsrc_t rs, int w0, int pieces, int run,
+                                int start, int rows) {
+        const int tid = threadIdx.x, row = tid >> 4, sub = tid & 15;
+        const auto slot = [&](int i) {   // a run that starts before this head ends with it: its second slot
+            const int w = w0 + i;
+            return (uint32_t)(2 * w + (w * run < start ? 1 : 0)) * a.slot_bytes;
+        };
+        float top = -INFINITY;
+        if (row < rows) {
+            for (int i = sub; i < pieces; i += 16) {
+                const uint32_t at = slot(i) + kRows * DPAD * 4 + row * 8;
+                const float pm = as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, kCacheSC1));
+                const float pl = as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at + 4, 0, kCacheSC1));
+                sh.join[row][i] = make_float2(pm, pl);
+                top = fmaxf(top, pm);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+            for (int i = sub; i < pieces; i += 16) {
+                const float2 p = sh.join[row][i];
+                const float w = __builtin_amdgcn_exp2f(p.x - base);
+                sh.join[row][i].x = w;
+                sum += w * p.y;
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d);
+            if (sub == 0) {
+                sh.row_m[row] = top;
+                sh.row_l[row] = sum;
+            }
+        }
+        __syncthreads();
+    }
+
+    static __device__ __forceinline__ void store4(const Args& a, int b, int head, int d, float4_t v, float by) {
+        uint16_t* p = a.out + b * a.out_row + head * a.out_head + d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = T::one(v[i] * by);
+    }
+
+    __device__ void run(const Args& a, Shared& sh) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
+
+        // the cut: units before every sequence, and the sequence of this run's first unit
+        const int each = (a.batch + 255) / 256;
+        int mine = 0, most = 0;
+        for (int i = 0; i < each; ++i) {
+            const int b = tid * each + i;
+            const int n = b < a.batch ? span_of(a.lengths[b], a).units : 0;
+            mine += n;
+            most = most > n ? most : n;
+        }
+        int scan = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(scan, d), other = __shfl_xor(most, d);
+            if (lane >= d) scan += up;
+            most = most > other ? most : other;
+        }
+        if (lane == 63) {
+            sh.scan[wave] = scan;
+            sh.most[wave] = most;
+        }
+        __syncthreads();
+        int total = 0, before = scan - mine;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += sh.scan[w];
+            total += sh.scan[w];
+            most = most > sh.most[w] ? most : sh.most[w];
+        }
+        total = uniform(total) * a.groups;
+        const int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+        const int least = (uniform(most) + kMaxPieces - 2) / (kMaxPieces - 1);
+        const int run = share > least ? share : least;
+        int u = (int)blockIdx.x * run;
+        if (u >= total) return;
+        const int end = u + run < total ? u + run : total;
+        for (int i = 0; i < each; ++i) {
+            const int b = tid * each + i;
+            const int n = b < a.batch ? span_of(a.lengths[b], a).units : 0;
+            if (before * a.groups <= u && u < (before + n) * a.groups) {
+                sh.found[0] = b;
+                sh.found[1] = before * a.groups;
+            }
+            before += n;
+        }
+        __syncthreads();
+        int b = uniform(sh.found[0]), base = uniform(sh.found[1]);
+        Span span = span_of(uniform(a.lengths[b]), a);
+        const __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc(a.partial, (short)0, (int)a.partial_bytes, 0x00020000);
+        int piece = 0;
+
+        while (u < end) {
+            const int h = (u - base) / span.units, c0 = u - base - h * span.units;
+            const int start = u - c0;
+            const int c1 = span.units < c0 + (end - u) ? span.units : c0 + (end - u);
+            const int kvh = h / a.tiles, tile = h - kvh * a.tiles;
+            const int rows = a.group - kRows * tile < kRows ? a.group - kRows * tile : kRows;
+            const int head0 = kvh * a.group + kRows * tile;
+            load_q(a, b, head0 + (c < rows ? c : 0), g);
+            float z_scale = a.scale * kLog2e;
+            if (a.softcap > 0.0f) z_scale = a.scale;
+            if (E4M3 && a.k_scale) z_scale *= a.k_scale[kvh];
+            m = -INFINITY;
+            l = 0.0f;
+#pragma unroll
+            for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                for (int r = 0; r < VW; ++r) o[nb][r] = float4_t{0, 0, 0, 0};
+            bool bad = span.bad;
+            const int32_t* pages = a.table + b * a.ld_table;
+            for (int i = c0; i < c1; ++i) {
+                const int t0 = span.first + i * kUnit + wave * kTile;
+                if (t0 < span.len) bad |= step(a, span, pages, kvh * a.k_head, kvh * a.v_head, t0, z_scale);
+            }
+            l = head_sum(l);
+            if (bad) l = NAN;
+
+            // the workgroup's wavefronts
+            if (g == 0) {
+                sh.m[wave][c] = m;
+                sh.l[wave][c] = l;
+            }
+            __syncthreads();
+            float top = sh.m[0][c];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.m[w][c]);
+            const float from = top == -INFINITY ? 0.0f : top;
+            const float by = __builtin_amdgcn_exp2f(m - from);
+            if (wave == 0 && g == 0) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) sum += sh.l[w][c] * __builtin_amdgcn_exp2f(sh.m[w][c] - from);
+                sh.row_m[c] = top;
+                sh.row_l[c] = sum;
+            }
+            const bool whole = c1 - c0 == span.units;
+            const float v_by = E4M3 && a.v_scale ? a.v_scale[kvh] : 1.0f;
+            const uint32_t slot = (uint32_t)(2 * (int)blockIdx.x + (piece ? 1 : 0)) * a.slot_bytes;
+#pragma unroll
+            for (int nb = 0; nb < VB; ++nb) {
+                if (nb) __syncthreads();
+                if (c < rows) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int r = 0; r < VW; r += 4)
+                            *reinterpret_cast<float4_t*>(&sh.o[wave][c][VW * (4 * g + i) + r]) =
+                                float4_t{o[nb][r][i] * by, o[nb][r + 1][i] * by, o[nb][r + 2][i] * by, o[nb][r + 3][i] * by};
+                }
+                __syncthreads();
+                for (int x = tid; x < rows * 4 * VW; x += 256) {
+                    const int row = x / (4 * VW), d = 4 * (x % (4 * VW));
+                    float4_t sum = *reinterpret_cast<const float4_t*>(&sh.o[0][row][d]);
+#pragma unroll
+                    for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const float4_t*>(&sh.o[w][row][d]);
+                    const int dim = nb * 16 * VW + d;
+                    if (whole) {
+                        const float total_l = sh.row_l[row];
+                        const bool none = span.len == 0 && !span.bad;
+                        if (dim < a.dim) store4(a, b, head0 + row, dim, sum, none ? 0.0f : v_by / total_l);
+                    } else {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, sum), rs,
+                                                               slot + (uint32_t)(row * DPAD + dim) * 4, 0, kCacheSC1);
+                    }
+                }
+            }
+            if (whole) {
+                if (a.lse && tid < rows)
+                    a.lse[(int64_t)b * a.heads + head0 + tid] =
+                        span.len == 0 && !span.bad ? -INFINITY
+                                                   : kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
+                __syncthreads();   // the next piece writes what this one reads
+            } else {
+                if (tid < rows) {
+                    const uint32_t at = slot + kRows * DPAD * 4 + tid * 8;
+                    __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_m[tid]), rs, at, 0, kCacheSC1);
+                    __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_l[tid]), rs, at + 4, 0, kCacheSC1);
+                }
+                __builtin_amdgcn_s_waitcnt(0);   // this thread's stores acknowledged
+                __syncthreads();                 // ... and every thread's, before the count
+                const int w0 = start / run, pieces = (start + span.units - 1) / run - w0 + 1;
+                uint32_t* counter = a.counters + (b * a.groups + h) * kCounterStep;
+                if (tid == 0)
+                    sh.last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                              (uint32_t)(pieces - 1);
+                __syncthreads();
+                if (uniform(sh.last)) {
+                    join(a, sh, rs, w0, pieces, run, start, rows);
+                    const int quads = a.dim / 4;
+                    for (int x = tid; x < rows * quads; x += 256) {
+                        const int row = x / quads, d = 4 * (x - row * quads);
+                        float4_t sum = {0, 0, 0, 0};
+                        for (int i = 0; i < pieces; i += 8) {
+                            uint4_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int at = i + k < pieces ? i + k : i, wg = w0 + at;
+                                const uint32_t s = (uint32_t)(2 * wg + (wg * run < start ? 1 : 0)) * a.slot_bytes;
+                                w[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, s + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (i + k < pieces) sum += __builtin_bit_cast(float4_t, w[k]) * sh.join[row][i + k].x;
+                        }
+                        store4(a, b, head0 + row, d, sum, v_by / sh.row_l[row]);
+                    }
+                    if (a.lse && tid < rows)
+                        a.lse[(int64_t)b * a.heads + head0 + tid] = kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
+                    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                }
+                __syncthreads();
+            }
+            u += c1 - c0;
+            ++piece;
+            if (u < end && u == base + a.groups * span.units) {
+                base = u;
+                ++b;
+                span = span_of(uniform(a.lengths[b]), a);
+            }
+        }
+    }
+};
+
+template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE>
+__global__ __launch_bounds__(256) void k_attn(Args a) {
+    using Op = Attention<T, E4M3, PAIRS, VW, VB, WHOLE>;
+    __shared__ typename Op::Shared sh;
+    Op op;
+    op.run(a, sh);
+}
+
+typedef void (*Kernel)(Args);
+
+template <class T, bool E4M3, bool WHOLE>
+Kernel pick_dim(int dim) {
+    if (dim <= 64) return k_attn<T, E4M3, 1, 4, 1, WHOLE>;
+    if (dim <= 128) return k_attn<T, E4M3, 2, 8, 1, WHOLE>;
+    if (dim <= 192) return k_attn<T, E4M3, 3, 4, 3, WHOLE>;
+    return k_attn<T, E4M3, 4, 8, 2, WHOLE>;
+}
+
+template <class T>
+Kernel pick(bool e4m3, bool whole, int dim) {
+    if (e4m3) return whole ? pick_dim<T, true, true>(dim) : pick_dim<T, true, false>(dim);
+    return whole ? pick_dim<T, false, true>(dim) : pick_dim<T, false, false>(dim);
+}
+
+int padded(int dim) { return (dim + 63) / 64 * 64; }
+uint32_t slot_bytes(int dim) { return (uint32_t)(kRows * padded(dim) * 4 + kRows * 8); }
+
+}  // namespace
+
+extern "C" size_t sgemv_attn_workspace_bytes(int32_t batch, int32_t heads, int32_t heads_kv, int32_t dim) {
+    if (batch < 0 || heads < 1 || heads > SGEMV_MAX_HEADS || heads_kv < 1 || heads % heads_kv || dim < 8 ||
+        dim > SGEMV_MAX_DIM || dim % 8)
+        return 0;
+    return kCounterBytes + (size_t)2 * kGrid * slot_bytes(dim);
+}
+
+extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cache, void* stream) {
+    if (!args || !cache) return SGEMV_EINVAL;
+    const sgemv_attn_args& p = *args;
+    const sgemv_kv& kv = *cache;
+    if (p.reserved || (p.type != SGEMV_F16 && p.type != SGEMV_BF16)) return SGEMV_EINVAL;
+    if (p.batch < 0 || p.heads < 1 || p.heads > SGEMV_MAX_HEADS) return SGEMV_ESIZE;
+    if (int e = sgemv_check_kv(kv)) return e;
+    if (kv.type != p.type && kv.type != SGEMV_E4M3) return SGEMV_EINVAL;
+    if (p.heads % kv.heads || !std::isfinite(p.scale) || !(p.softcap >= 0.0f) || std::isinf(p.softcap)) return SGEMV_EINVAL;
+    if (p.window < 0 || p.max_pages < 1 || (int64_t)p.max_pages * kv.page_size > 0x7FFFFFFF - 256) return SGEMV_ESIZE;
+    if (p.batch == 0) return SGEMV_OK;
+    if (!p.q || !p.out || !p.table || !p.lengths || !p.workspace) return SGEMV_EINVAL;
+    const int64_t most = (int64_t)1 << 40;
+    if (p.ld_table < p.max_pages || p.ld_table > most || p.q_row < 0 || p.q_head < 0 || p.out_row < 0 || p.out_head < 0 ||
+        p.q_row > most || p.q_head > most || p.out_row > most || p.out_head > most)
+        return SGEMV_ESIZE;
+    if ((p.heads > 1 && (p.q_head < kv.dim || p.out_head < kv.dim)) ||
+        (p.batch > 1 && (p.q_row < kv.dim || p.out_row < kv.dim)))
+        return SGEMV_ESIZE;
+    // rows outside of heads or heads outside of rows; nothing of out is written twice
+    const int64_t heads_span = (int64_t)(p.heads - 1) * p.out_head + kv.dim, rows_span = (int64_t)(p.batch - 1) * p.out_row + kv.dim;
+    if (p.batch > 1 && p.heads > 1 && p.out_row < heads_span && p.out_head < rows_span) return SGEMV_ESIZE;
+    const size_t need = sgemv_attn_workspace_bytes(p.batch, p.heads, kv.heads, kv.dim);
+    if (p.workspace_bytes < need) return SGEMV_ESIZE;
+    if (!sgemv_aligned(p.q, 2) || !sgemv_aligned(p.out, 2) || !sgemv_aligned(p.lse, 4) || !sgemv_aligned(p.table, 4) ||
+        !sgemv_aligned(p.lengths, 4) || !sgemv_aligned(p.workspace, 256))
+        return SGEMV_EALIGN;
+    const auto whole = [&](const void* at, int64_t row, int64_t head) {
+        return SgemvRows{at, 1, 0, ((int64_t)(p.batch - 1) * row + (int64_t)(p.heads - 1) * head + kv.dim) * 2};
+    };
+    const SgemvRows q = whole(p.q, p.q_row, p.q_head), out = whole(p.out, p.out_row, p.out_head);
+    const SgemvRows lse = {p.lse, 1, 0, (int64_t)p.batch * p.heads * 4};
+    const SgemvRows ins[] = {{p.table, 1, 0, ((int64_t)(p.batch - 1) * p.ld_table + p.max_pages) * 4},
+                             {p.lengths, 1, 0, (int64_t)p.batch * 4},
+                             {p.workspace, 1, 0, (int64_t)need},
+                             {kv.k_scale, 1, 0, kv.heads * 4},
+                             {kv.v_scale, 1, 0, kv.heads * 4},
+                             sgemv_kv_rows(kv, true),
+                             sgemv_kv_rows(kv, false),
+                             q};
+    if (sgemv_overlap(out, lse)) return SGEMV_EINVAL;
+    for (const SgemvRows& in : ins)
+        if (sgemv_overlap(out, in) || sgemv_overlap(lse, in)) return SGEMV_EINVAL;
+
+    const int es = kv.type == SGEMV_E4M3 ? 1 : 2;
+    Args a;
+    a.k = static_cast<const uint8_t*>(kv.k);
+    a.v = static_cast<const uint8_t*>(kv.v);
+    a.k_scale = kv.k_scale;
+    a.v_scale = kv.v_scale;
+    a.k_page = kv.k_page * es; a.k_token = kv.k_token * es; a.k_head = kv.k_head * es;
+    a.v_page = kv.v_page * es; a.v_token = kv.v_token * es; a.v_head = kv.v_head * es;
+    a.counters = static_cast<uint32_t*>(p.workspace);
+    a.partial = static_cast<uint8_t*>(p.workspace) + kCounterBytes;
+    a.q_row = p.q_row; a.q_head = p.q_head; a.out_row = p.out_row; a.out_head = p.out_head; a.ld_table = p.ld_table;
+    a.page = sgemv_div(kv.page_size);
+    a.pages = kv.pages;
+    a.capacity = p.max_pages * kv.page_size;
+    a.heads = p.heads;
+    a.group = p.heads / kv.heads;
+    a.tiles = (a.group + kRows - 1) / kRows;
+    a.groups = kv.heads * a.tiles;
+    a.dim = kv.dim;
+    a.window = p.window;
+    a.q_vector = sgemv_aligned(p.q, 16) && p.q_row % 8 == 0 && p.q_head % 8 == 0;
+    a.slot_bytes = slot_bytes(kv.dim);
+    a.partial_bytes = 2 * kGrid * a.slot_bytes;
+    a.scale = p.scale;
+    a.softcap = p.softcap;
+    const bool whole_pages = kv.page_size % 16 == 0, e4m3 = kv.type == SGEMV_E4M3;
+    const Kernel kernel = p.type == SGEMV_F16 ? pick<F16>(e4m3, whole_pages, kv.dim) : pick<BF16>(e4m3, whole_pages, kv.dim);
+    // a launch counts its units in 30 bits and its heads by kMaxHeads counters
+    const int64_t units = (int64_t)a.groups * (a.capacity / kUnit + 2);
+    int64_t per = kMaxHeads / a.groups;
+    if (per > 0x3FFFFFFF / units) per = 0x3FFFFFFF / units;
+    if (per < 1) return SGEMV_ESIZE;
+    for (int64_t b = 0; b < p.batch; b += per) {
+        a.batch = (int)(p.batch - b < per ? p.batch - b : per);
+        a.q = static_cast<const uint16_t*>(p.q) + b * p.q_row;
+        a.out = static_cast<uint16_t*>(p.out) + b * p.out_row;
+        a.lse = p.lse ? p.lse + b * p.heads : nullptr;
+        a.table = p.table + b * p.ld_table;
+        a.lengths = p.lengths + b;
+        void* kargs[] = {&a};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(kGrid), dim3(256), kargs, 0,
+                                             static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return sgemv_hip_failed((int)e);
+    }
+    return SGEMV_OK;
+}

@@ -35,6 +35,11 @@ SGEMV_F16, SGEMV_BF16, SGEMV_F32 = 0, 1, 2
 SGEMV_ACT_SILU, SGEMV_ACT_GELU, SGEMV_ACT_RELU = 0, 1, 2
 SGEMV_Q4_GATED, SGEMV_Q4_ZEROS, SGEMV_Q4_BF16_SCALES = 1, 2, 4
 SGEMV_NORM_POST, SGEMV_NORM_CENTER, SGEMV_NORM_PLUS_ONE = 1, 2, 4
+SGEMV_E4M3 = 3
+SGEMV_ROTARY_ADJACENT, SGEMV_ROTARY_STRIPED = 1, 2
+SGEMV_MAX_HEADS, SGEMV_MAX_DIM, SGEMV_MAX_AXES = 1024, 256, 4
+SGEMV_MAX_BEAMS, SGEMV_MAX_CHOICES = 32, 64
+SGEMV_MAX_LAYERS, SGEMV_MAX_ROWS = 128, 8192
 
 EXPORTED = ["sgemv_pack_layout", "sgemv_pack_layout_z4", "sgemv_pack_layout_ng", "sgemv_pack_layout_parts",
             "sgemv_desc_from_header",
@@ -43,6 +48,9 @@ EXPORTED = ["sgemv_pack_layout", "sgemv_pack_layout_z4", "sgemv_pack_layout_ng",
             "sgemv_q4_pack", "sgemv_q4_pack_gated", "sgemv_q4_pack_device",
             "sgemv_q4_desc_from_header", "sgemv_q4_run", "sgemv_q4_run_gated",
             "sgemv_block_norm",
+            "sgemv_rotary", "sgemv_attn_paged", "sgemv_attn_workspace_bytes",
+            "sgemv_beam_select", "sgemv_beam_workspace_bytes",
+            "sgemv_pages_fork", "sgemv_pages_compact", "sgemv_pages_copy", "sgemv_pages_workspace_bytes",
             "sgemv_strerror", "sgemv_last_hip_error"]
 
 
@@ -124,6 +132,18 @@ def lib():
     L.sgemv_q4_run_gated.restype = ctypes.c_int
     L.sgemv_block_norm.argtypes = [ctypes.c_char_p, vp]
     L.sgemv_block_norm.restype = ctypes.c_int
+    raw = ctypes.c_char_p   # a packed struct
+    for name in ("sgemv_rotary", "sgemv_attn_paged", "sgemv_pages_fork", "sgemv_pages_compact"):
+        getattr(L, name).argtypes = [raw, raw, vp]
+        getattr(L, name).restype = ctypes.c_int
+    L.sgemv_beam_select.argtypes = [raw, vp]
+    L.sgemv_beam_select.restype = ctypes.c_int
+    L.sgemv_pages_copy.argtypes = [raw, i32, vp, vp, i32, vp]
+    L.sgemv_pages_copy.restype = ctypes.c_int
+    for name, n in (("sgemv_attn_workspace_bytes", 4), ("sgemv_beam_workspace_bytes", 4),
+                    ("sgemv_pages_workspace_bytes", 3)):
+        getattr(L, name).argtypes = [i32] * n
+        getattr(L, name).restype = sz
     L.sgemv_strerror.argtypes = [ctypes.c_int]
     L.sgemv_strerror.restype = ctypes.c_char_p
     L.sgemv_last_hip_error.argtypes = []
@@ -434,6 +454,7 @@ def sgemv_run_fused_static(desc: Desc, packed, x, thresholds, y, idx=None, count
 # 4-bit products that read every weight, and the norms around a block
 # ---------------------------------------------------------------------------
 _TYPES: dict = {}     # torch dtype -> SGEMV_F16 / BF16 / F32, filled on the first call
+_CACHE_TYPES: dict = {}
 _torch = None
 _raw_stream = None    # device index -> handle of its current stream
 _device_now = None    # -> index of the current device
@@ -445,6 +466,7 @@ def _load_torch():
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
     _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
+    _CACHE_TYPES.update({torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float8_e4m3fn: SGEMV_E4M3})
     # last: a thread that finds its type here uses the others without a check
     _TYPES.update({torch.float16: SGEMV_F16, torch.bfloat16: SGEMV_BF16, torch.float32: SGEMV_F32})
 
@@ -867,6 +889,337 @@ def sgemv_block_norm(x, residual, y=None, residual_out=None, *, weight=None, bia
     device = residual.device
     args = _NORM.pack(rows, D, flags, *addresses, *strides, scale, eps, *types)
     _call(lib().sgemv_block_norm, device, (args, _stream_on(device, stream)), "sgemv_block_norm")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, a paged cache, attention over it, beams, pages
+# ---------------------------------------------------------------------------
+# the C header's structs, field by field
+_KV = struct.Struct("@4P6q6i")
+_ROTARY = struct.Struct("@8P12q10iIf")
+_ATTN = struct.Struct("@6PN5q5i2fi")
+_BEAM = struct.Struct("@7PN2q6i")
+_PAGES = struct.Struct("@13PN2q6i")
+
+
+class KVCache:
+    """One layer's paged cache over the caller's tensors: k and v are
+    [pages][page_size][heads][dim] in float16, bfloat16 or float8_e4m3fn, any
+    strides with the last dimension contiguous (a [pages][heads][page_size][dim]
+    buffer is passed as buffer.transpose(1, 2), keys and values of one buffer as
+    its slices).  k_scale and v_scale, float32 [heads], say what a stored 1 of
+    an 8-bit cache stands for (None: 1)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not _TYPES:
+            _load_torch()
+        for what, t in (("k", k), ("v", v)):
+            if not isinstance(t, _torch.Tensor) or t.dim() != 4:
+                raise ValueError(f"{what}: expected a torch tensor [pages][page_size][heads][dim]")
+            if t.dtype not in _CACHE_TYPES:
+                raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected float16, bfloat16, "
+                                 "float8_e4m3fn")
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{what}: the last dimension must be contiguous")
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v: must have one shape and type")
+        self.pages, self.page_size, self.heads, self.dim = k.shape
+        _fits_int32("KVCache", pages=self.pages, page_size=self.page_size, heads=self.heads, dim=self.dim)
+        self.type = _CACHE_TYPES[k.dtype]
+        at = []
+        for what, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and self.type != SGEMV_E4M3:
+                raise ValueError(f"{what}: for float8_e4m3fn caches only")
+            at.append(0 if t is None else _vector(t, what, self.heads, SGEMV_F32))
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        for t in (v, k_scale, v_scale):
+            if t is not None and t.device != self.device:
+                raise ValueError("k, v and their scales: must be on one device")
+        self.args = _KV.pack(k.data_ptr(), v.data_ptr(), *at, *k.stride()[:3], *v.stride()[:3], self.type, self.pages,
+                             self.page_size, self.heads, self.dim, 0)
+
+
+def _cache(cache) -> KVCache:
+    if not isinstance(cache, KVCache):
+        raise ValueError(f"cache: expected a KVCache, got {type(cache).__name__}")
+    return cache
+
+
+def _heads_of(t, what: str, code: int, like=None):
+    """(address, row stride, head stride) of a [rows][heads][dim] tensor of
+    type `code`, of the shape `like` where that is given."""
+    try:
+        if _TYPES[t.dtype] == code:
+            shape, (row, head, one) = t.shape, t.stride()
+            if (one == 1 or shape[2] <= 1) and (like is None or shape == like):
+                return t.data_ptr(), row, head
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
+    if _type_code(t, what) != code:
+        raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')} differs from the operands it goes with")
+    if t.dim() != 3 or (like is not None and t.shape != like):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {'[rows][heads][dim]' if like is None else tuple(like)}")
+    raise ValueError(f"{what}: the last dimension must be contiguous")
+
+
+def _ints(t, what: str, *shape) -> int:
+    """Address of a contiguous int32 tensor of `shape` (None: any size)."""
+    if not isinstance(t, _torch.Tensor):
+        raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype is not _torch.int32:
+        raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected int32")
+    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {''.join('[any]' if n is None else f'[{n}]' for n in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _table_of(t, what: str, rows: int):
+    """(address, row stride, columns) of an int32 [rows][max_pages] table."""
+    if not isinstance(t, _torch.Tensor):
+        raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
+    if t.dtype is not _torch.int32:
+        raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected int32")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{rows}][max_pages]")
+    (ld, one), columns = t.stride(), t.shape[1]
+    if columns > 1 and one != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), max(ld, columns) if rows <= 1 else ld, columns
+
+
+def _space(t):
+    """(address, bytes) of a workspace."""
+    if not isinstance(t, _torch.Tensor) or t.dtype is not _torch.uint8 or not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor")
+    return t.data_ptr(), t.numel()
+
+
+def sgemv_rotary(q, q_out, positions, inv_freq, *, k=None, k_out=None, v=None, cache: KVCache | None = None, slots=None,
+                 sections=None, adjacent: bool = False, striped: bool = False, scale: float = 1.0, stream=None):
+    """Turn q (and k) by their positions, write k and v into a paged cache.
+    q, q_out are [tokens][heads][dim], k, k_out, v [tokens][kv heads][dim], of
+    one type (float16, bfloat16, float32), any strides with the last dimension
+    contiguous (views of one projection's output); q and q_out may be None, and
+    an output may be its input.  positions is int32 [tokens] or [axes][tokens],
+    inv_freq float32 [pairs]; sections gives each axis its number of pairs
+    (None: one axis), dealt in turn when `striped`.  Pairs are (i, pairs + i)
+    of a head, or (2i, 2i + 1) when `adjacent`.  With a cache, slots is int32
+    [tokens] (page * page_size + place; negative: not written)."""
+    first = q if q is not None else k
+    code = _type_code(first, "q" if q is not None else "k")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    if first.dim() != 3:
+        raise ValueError(f"{'q' if q is not None else 'k'}: shape {tuple(first.shape)}, expected [tokens][heads][dim]")
+    tokens, _, dim = first.shape
+    at, strides = [0] * 8, [0] * 11
+    if q is not None:
+        at[0], strides[0], strides[1] = _heads_of(q, "q", code)
+        at[1], strides[2], strides[3] = _heads_of(q_out, "q_out", code, q.shape)
+    if k is not None:
+        at[2], strides[4], strides[5] = _heads_of(k, "k", code)
+        if k.shape[0] != tokens or k.shape[2] != dim:
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected [{tokens}][kv heads][{dim}]")
+        if k_out is not None:
+            at[3], strides[6], strides[7] = _heads_of(k_out, "k_out", code, k.shape)
+        elif cache is None:
+            raise ValueError("k: needs k_out or a cache")
+    elif k_out is not None:
+        raise ValueError("k_out: needs k")
+    if cache is None:
+        if v is not None or slots is not None:
+            raise ValueError("v, slots: need a cache")
+    else:
+        if k is None:
+            raise ValueError("cache: needs k")
+        if (_cache(cache).heads, cache.dim) != (k.shape[1], dim):
+            raise ValueError(f"cache: {cache.heads} heads of {cache.dim}, k has {k.shape[1]} of {dim}")
+        if v is not None:
+            at[4], strides[8], strides[9] = _heads_of(v, "v", code, k.shape)
+        at[7] = _ints(slots, "slots", tokens)
+    if not isinstance(positions, _torch.Tensor) or positions.dtype is not _torch.int32 or positions.dim() not in (1, 2) \
+            or positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions: expected int32 [{tokens}] or [axes][{tokens}], the last dimension contiguous")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    at[5], strides[10] = positions.data_ptr(), max(positions.stride(0), tokens) if axes == 1 else positions.stride(0)
+    if _type_code(inv_freq, "inv_freq") != SGEMV_F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq: expected float32 [pairs], contiguous")
+    at[6], pairs = inv_freq.data_ptr(), inv_freq.shape[0]
+    sections = [pairs] if sections is None else list(sections)
+    if len(sections) != axes or axes > SGEMV_MAX_AXES or sum(sections) != pairs or min(sections, default=-1) < 0:
+        raise ValueError(f"sections: {sections}, expected {axes} numbers that sum to {pairs} (up to {SGEMV_MAX_AXES})")
+    _fits_int32("sgemv_rotary", tokens=tokens)
+    device = first.device
+    _on_one_gpu(device, ("q", "q_out", "k", "k_out", "v", "positions", "inv_freq", "slots", "cache"),
+                (q, q_out, k, k_out, v, positions, inv_freq, slots, None if cache is None else cache.k))
+    args = _ROTARY.pack(*at, *strides, tokens, code, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim,
+                        pairs, axes, *sections, *[0] * (SGEMV_MAX_AXES - axes),
+                        (SGEMV_ROTARY_ADJACENT if adjacent else 0) | (SGEMV_ROTARY_STRIPED if striped else 0), scale)
+    _call(lib().sgemv_rotary, device, (args, None if cache is None else cache.args, _stream_on(device, stream)),
+          "sgemv_rotary")
+
+
+def sgemv_attn_workspace_bytes(batch: int, heads: int, heads_kv: int, dim: int) -> int:
+    return int(lib().sgemv_attn_workspace_bytes(batch, heads, heads_kv, dim))
+
+
+def sgemv_attn_paged(q, cache: KVCache, table, lengths, out, workspace, *, scale: float | None = None, window: int = 0,
+                     softcap: float = 0.0, lse=None, stream=None):
+    """Attention of one new token per sequence over its paged cache: q and out
+    are [batch][heads][dim] in float16 or bfloat16, heads a multiple of the
+    cache's; table is int32 [batch][max_pages], lengths int32 [batch], both on
+    the device; workspace is uint8, zero-filled once, of
+    sgemv_attn_workspace_bytes(batch, heads, kv heads, dim).  scale defaults
+    to 1 / sqrt(dim); window: only the last tokens are seen (0: all);
+    softcap * tanh(z / softcap) of every score (0: none); lse (optional)
+    float32 [batch][heads] receives the logarithm of the sum of exponentials."""
+    code = _type_code(q, "q")
+    if code == SGEMV_F32:
+        raise ValueError("q: dtype float32, expected float16, bfloat16")
+    qp, q_row, q_head = _heads_of(q, "q", code)
+    op, out_row, out_head = _heads_of(out, "out", code, q.shape)
+    batch, heads, dim = q.shape
+    if _cache(cache).dim != dim or heads % cache.heads:
+        raise ValueError(f"cache: {cache.heads} heads of {cache.dim}, q has {heads} of {dim}")
+    if cache.type not in (code, SGEMV_E4M3):
+        raise ValueError("cache: must have q's type, or float8_e4m3fn")
+    tp, ld, columns = _table_of(table, "table", batch)
+    lp, zp = _ints(lengths, "lengths", batch), 0
+    if lse is not None:
+        if _type_code(lse, "lse") != SGEMV_F32 or lse.shape != (batch, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse: expected float32 [{batch}][{heads}], contiguous")
+        zp = lse.data_ptr()
+    wp, size = _space(workspace)
+    _fits_int32("sgemv_attn_paged", batch=batch, heads=heads, max_pages=columns, window=window)
+    device = q.device
+    _on_one_gpu(device, ("q", "cache", "table", "lengths", "out", "workspace", "lse"),
+                (q, cache.k, table, lengths, out, workspace, lse))
+    args = _ATTN.pack(qp, op, zp, tp, lp, wp, size, q_row, q_head, out_row, out_head, ld, code, batch, heads, columns,
+                      window, dim ** -0.5 if scale is None else scale, softcap, 0)
+    _call(lib().sgemv_attn_paged, device, (args, cache.args, _stream_on(device, stream)), "sgemv_attn_paged")
+
+
+def sgemv_beam_workspace_bytes(batch: int, beams: int, vocab: int, choices: int) -> int:
+    return int(lib().sgemv_beam_workspace_bytes(batch, beams, vocab, choices))
+
+
+def sgemv_beam_select(logits, scores, tokens, parents, scores_out, workspace, *, finished=None, end_token: int = 0,
+                      stream=None):
+    """The best continuations of a batch of beam searches: logits
+    [batch][beams][vocab] (float16, bfloat16, float32, any strides with the
+    last dimension contiguous), scores float32 [batch][beams]; tokens and
+    parents int32 and scores_out float32 [batch][choices] receive the largest
+    score + log softmax(logits), largest first.  finished (optional) uint8
+    [batch][beams]: such a beam goes on with end_token at its own score.
+    workspace is uint8, zero-filled once, of sgemv_beam_workspace_bytes(batch,
+    beams, vocab, choices)."""
+    code = _type_code(logits, "logits")
+    lp, ld_batch, ld_beam = _heads_of(logits, "logits", code)
+    batch, beams, vocab = logits.shape
+    if not isinstance(scores_out, _torch.Tensor) or scores_out.dim() != 2:
+        raise ValueError(f"scores_out: expected float32 [{batch}][choices]")
+    choices = scores_out.shape[1]
+    for what, t, shape in (("scores", scores, (batch, beams)), ("scores_out", scores_out, (batch, choices))):
+        if _type_code(t, what) != SGEMV_F32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{what}: expected float32 {shape}, contiguous")
+    fp = 0
+    if finished is not None:
+        if not isinstance(finished, _torch.Tensor) or finished.dtype not in (_torch.uint8, _torch.bool) \
+                or finished.shape != (batch, beams) or not finished.is_contiguous():
+            raise ValueError(f"finished: expected uint8 or bool [{batch}][{beams}], contiguous")
+        fp = finished.data_ptr()
+    wp, size = _space(workspace)
+    _fits_int32("sgemv_beam_select", batch=batch, beams=beams, vocab=vocab, choices=choices, end_token=end_token)
+    device = logits.device
+    args = _BEAM.pack(lp, scores.data_ptr(), fp, _ints(tokens, "tokens", batch, choices),
+                      _ints(parents, "parents", batch, choices), scores_out.data_ptr(), wp, size, ld_batch, ld_beam, code,
+                      batch, beams, vocab, choices, end_token)
+    _on_one_gpu(device, ("logits", "scores", "tokens", "parents", "scores_out", "workspace", "finished"),
+                (logits, scores, tokens, parents, scores_out, workspace, finished))
+    _call(lib().sgemv_beam_select, device, (args, _stream_on(device, stream)), "sgemv_beam_select")
+
+
+def sgemv_pages_workspace_bytes(rows: int, max_pages: int, pages: int) -> int:
+    return int(lib().sgemv_pages_workspace_bytes(rows, max_pages, pages))
+
+
+def _caches(caches) -> tuple:
+    caches = [_cache(c) for c in caches]
+    if len(caches) > SGEMV_MAX_LAYERS:
+        raise SgemvError(SGEMV_ESIZE, f"caches: {len(caches)}, at most {SGEMV_MAX_LAYERS} a call")
+    return caches, b"".join([c.args for c in caches]) if caches else None
+
+
+def _pages_call(name, table, lengths, refs, table_out, lengths_out, refs_out, workspace, page_size, parents, grow, slots,
+                pairs, count, status, caches, stream):
+    if not _TYPES:
+        _load_torch()
+    if not isinstance(table, _torch.Tensor) or table.dim() != 2:
+        raise ValueError("table: expected int32 [rows][max_pages]")
+    rows = table.shape[0]
+    tp, ld, columns = _table_of(table, "table", rows)
+    op, ld_out, columns_out = _table_of(table_out, "table_out", rows)
+    if columns_out != columns:
+        raise ValueError(f"table_out: {columns_out} columns, table has {columns}")
+    lp, rp = _ints(lengths, "lengths", rows), _ints(refs, "refs", None)
+    pages = refs.shape[0]
+    fork = name == "sgemv_pages_fork"
+    at = [tp, lp, rp, op, _ints(lengths_out, "lengths_out", rows) if fork else 0, _ints(refs_out, "refs_out", pages),
+          0 if parents is None else _ints(parents, "parents", rows), 0 if grow is None else _ints(grow, "grow", rows),
+          0 if slots is None else _ints(slots, "slots", rows, None), _ints(pairs, "pairs", rows if fork else pages, 3),
+          _ints(count, "count", 1), _ints(status, "status", 2) if fork else 0]
+    wp, size = _space(workspace)
+    max_grow = 0 if slots is None else slots.shape[1]
+    _fits_int32(name, rows=rows, max_pages=columns, pages=pages, page_size=page_size, max_grow=max_grow)
+    caches, packed = _caches(caches)
+    device = table.device
+    _on_one_gpu(device, ("table", "lengths", "refs", "table_out", "lengths_out", "refs_out", "parents", "grow", "slots",
+                         "pairs", "count", "status", "workspace") + ("caches",) * len(caches),
+                (table, lengths, refs, table_out, lengths_out, refs_out, parents, grow, slots, pairs, count, status,
+                 workspace) + tuple(c.k for c in caches))
+    args = _PAGES.pack(*at, wp, size, ld, ld_out, rows, columns, pages, page_size, max_grow, len(caches))
+    _call(getattr(lib(), name), device, (args, packed, _stream_on(device, stream)), name)
+
+
+def sgemv_pages_fork(table, lengths, refs, table_out, lengths_out, refs_out, workspace, *, page_size: int, pairs, count,
+                     status, parents=None, grow=None, slots=None, caches=(), stream=None):
+    """One step of a batch's pages, all int32 on the device: table
+    [rows][max_pages], lengths [rows], refs [pages] (how many rows' entries name
+    a page; 0: free).  Row r takes over the pages of row parents[r] (None: its
+    own; outside 0 .. rows - 1: it ends), then grows by grow[r] tokens (None: by
+    none), whose places go to slots [rows][most]; a shared last page is copied
+    for a row that grows, in every KVCache of `caches`, and listed in pairs
+    [rows][3], count [1].  status [2]: pages missing, rows that cannot grow
+    that far; where either is not 0, no row grows.  Outputs may be their inputs.
+    workspace is uint8, zero-filled once, of sgemv_pages_workspace_bytes."""
+    _pages_call("sgemv_pages_fork", table, lengths, refs, table_out, lengths_out, refs_out, workspace, page_size, parents,
+                grow, slots, pairs, count, status, caches, stream)
+
+
+def sgemv_pages_compact(table, lengths, refs, table_out, refs_out, workspace, *, page_size: int, pairs, count, caches=(),
+                        stream=None):
+    """Move the pages in use to the lowest ids, in tables, counts and every
+    KVCache of `caches`; pairs [pages][3] and count [1] say which went where."""
+    _pages_call("sgemv_pages_compact", table, lengths, refs, table_out, None, refs_out, workspace, page_size, None, None,
+                None, pairs, count, None, caches, stream)
+
+
+def sgemv_pages_copy(caches, pairs, count=None, stream=None):
+    """Copy pages within every KVCache of `caches`: pairs int32 [n][3] of
+    (source, target, tokens), the first count[0] of them (None: all)."""
+    if not _TYPES:
+        _load_torch()
+    caches, packed = _caches(caches)
+    if not caches:
+        raise ValueError("caches: at least one")
+    pp, cp = _ints(pairs, "pairs", None, 3), 0 if count is None else _ints(count, "count", 1)
+    _fits_int32("sgemv_pages_copy", pairs=pairs.shape[0])
+    device = caches[0].device
+    _on_one_gpu(device, ("caches",) * len(caches) + ("pairs", "count"), tuple(c.k for c in caches) + (pairs, count))
+    _call(lib().sgemv_pages_copy, device, (packed, len(caches), pp, cp, pairs.shape[0], _stream_on(device, stream)),
+          "sgemv_pages_copy")
 
 
 def sgemv_workspace_bytes(desc: Desc, M: int = 1) -> int:

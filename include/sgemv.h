@@ -395,7 +395,9 @@ size_t sgemv_workspace_bytes(const sgemv_desc* d, int32_t M);
 enum sgemv_type {            /* element types of x, y, residuals and weights */
     SGEMV_F16  = 0,
     SGEMV_BF16 = 1,
-    SGEMV_F32  = 2
+    SGEMV_F32  = 2,
+    SGEMV_E4M3 = 3           /* 8 bits (4 exponent, 3 mantissa; no infinity,
+                                largest value 448): caches only              */
 };
 
 enum sgemv_act {             /* gate functions of sgemv_q4_run_gated         */
@@ -591,6 +593,273 @@ typedef struct sgemv_norm {
  * rows, D or a stride; EALIGN for pointers.
  */
 int sgemv_block_norm(const sgemv_norm* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Between the projections and the next token: rotary positions, a paged cache
+ * of keys and values, attention of one new token over it, beam selection, and
+ * the cache's pages.
+ *
+ * The conventions are those above: the caller owns every buffer, arguments
+ * are checked before any HIP call, work is enqueued on `stream` on the current
+ * device, results are bitwise reproducible, and every call may be captured
+ * into a graph.  Calls with a workspace take one that is zero-filled once by
+ * the caller; they leave its counters at zero again, so it serves any number
+ * of later calls of any shape it is large enough for, one after the other:
+ * calls that share a workspace (graphs that were captured with the same one
+ * among them) must not run at the same time.
+ * ------------------------------------------------------------------------ */
+
+#define SGEMV_MAX_HEADS   1024
+#define SGEMV_MAX_DIM     256
+#define SGEMV_MAX_AXES    4
+#define SGEMV_MAX_BEAMS   32
+#define SGEMV_MAX_CHOICES 64
+#define SGEMV_MAX_LAYERS  128
+#define SGEMV_MAX_ROWS    8192
+
+/* One layer's paged cache (host memory).  The key of the token at place
+ * `slot = page * page_size + t` and head h is the dim values at
+ *   k + page * k_page + t * k_token + h * k_head,
+ * its value likewise; a sequence's pages are listed by a table, its token i
+ * in page table[i / page_size] at t = i % page_size.  Strides are in elements
+ * and may be in any order (heads inside or outside of tokens, keys and values
+ * in one buffer); they and the addresses are multiples of 16 bytes, or of 8
+ * for SGEMV_E4M3. */
+typedef struct sgemv_kv {
+    void*        k;
+    void*        v;
+    const float* k_scale;    /* device [heads], SGEMV_E4M3 only: what a stored
+                                1 stands for; NULL: 1                         */
+    const float* v_scale;
+    int64_t      k_page, k_token, k_head, v_page, v_token, v_head;
+    int32_t      type;       /* SGEMV_F16, SGEMV_BF16 or SGEMV_E4M3           */
+    int32_t      pages;      /* 1 ..; pages * page_size < 2^31                */
+    int32_t      page_size;  /* 1 .. 65536, any number                        */
+    int32_t      heads;      /* 1 .. SGEMV_MAX_HEADS                          */
+    int32_t      dim;        /* 8 .. SGEMV_MAX_DIM, a multiple of 8           */
+    int32_t      reserved;   /* 0                                             */
+} sgemv_kv;
+
+#define SGEMV_ROTARY_ADJACENT 1u  /* pairs (2i, 2i+1); else (i, pairs + i)    */
+#define SGEMV_ROTARY_STRIPED  2u  /* pairs are dealt to the axes in turn      */
+
+/* Arguments of sgemv_rotary (host memory, read during the call). */
+typedef struct sgemv_rotary_args {
+    const void*    q;          /* device [tokens][heads_q][dim] of type, or NULL */
+    void*          q_out;
+    const void*    k;          /* device [tokens][heads_kv][dim], or NULL       */
+    void*          k_out;      /* may be NULL when a cache is given             */
+    const void*    v;          /* NULL, or given with a cache                   */
+    const int32_t* positions;  /* device [axes][ld_positions]                   */
+    const float*   inv_freq;   /* device [pairs]                                */
+    const int32_t* slots;      /* device [tokens], with a cache                 */
+    int64_t        q_row, q_head, q_out_row, q_out_head, k_row, k_head, k_out_row,
+                   k_out_head, v_row, v_head, ld_positions;   /* in elements    */
+    int64_t        tokens;     /* 0 ..                                          */
+    int32_t        type;       /* SGEMV_F16, SGEMV_BF16 or SGEMV_F32            */
+    int32_t        heads_q, heads_kv, dim;
+    int32_t        pairs;      /* 1 .. dim / 2                                  */
+    int32_t        axes;       /* 1 .. SGEMV_MAX_AXES                           */
+    int32_t        sections[SGEMV_MAX_AXES];  /* pairs of each axis, >= 0, their
+                                  sum is pairs                                  */
+    uint32_t       flags;      /* SGEMV_ROTARY_*                                */
+    float          scale;      /* factor of cosine and sine, finite             */
+} sgemv_rotary_args;
+
+/*
+ * sgemv_rotary - turn the queries and keys of `tokens` tokens by their
+ * positions, and write the keys and values into a paged cache, in one launch:
+ *   angle(t, i) = positions[axis(i)][t] * inv_freq[i]          i < pairs
+ *   (a, b) -> scale * (a cos - b sin, a sin + b cos)
+ * for the pair (a, b) of elements (i, pairs + i) of a head, or (2i, 2i+1) with
+ * SGEMV_ROTARY_ADJACENT; elements from 2 * pairs on pass as they are.  axis(i)
+ * is 0 for the first sections[0] pairs, 1 for the next sections[1], and so on;
+ * with SGEMV_ROTARY_STRIPED pairs go to axes 0, 1, ... in turn, leaving out
+ * axes that have all of theirs.  Angles are taken in 64 bits (positions are
+ * exact up to 2^31), cosine, sine and the turn in 32, each result rounded once.
+ *   q -> q_out; k -> k_out (optional) and, with a cache `kv`, to its slot;
+ *   v -> its slot as it is.  A slot below 0 or beyond the cache writes
+ *   nothing.  With SGEMV_E4M3 the cache holds value / scale of the head,
+ *   rounded to nearest even and held at +-448; NaN stays NaN.
+ * Two tokens with one slot leave either one's values there.
+ * q_out and k_out may be q and k themselves (same address and strides); any
+ * other overlap of an output with another operand is refused.  Operands need
+ * the alignment of their elements (16-byte addresses and strides are faster).
+ * EINVAL for NULL, a bad type, flag or section, an overlap; ESIZE for sizes and
+ * strides (positions: ld_positions >= tokens); EALIGN for pointers, and for a
+ * cache's strides; EINVAL too where kv and the arguments differ in heads or dim.
+ */
+int sgemv_rotary(const sgemv_rotary_args* a, const sgemv_kv* kv, void* stream);
+
+/* Arguments of sgemv_attn_paged (host memory, read during the call). */
+typedef struct sgemv_attn_args {
+    const void*    q;          /* device [batch][heads][dim] of type             */
+    void*          out;        /* device [batch][heads][dim] of type             */
+    float*         lse;        /* device [batch][heads], or NULL                 */
+    const int32_t* table;      /* device [batch][ld_table], max_pages used       */
+    const int32_t* lengths;    /* device [batch]                                 */
+    void*          workspace;  /* device, 256-byte aligned, zero-filled once     */
+    size_t         workspace_bytes;
+    int64_t        q_row, q_head, out_row, out_head, ld_table;   /* in elements  */
+    int32_t        type;       /* SGEMV_F16 or SGEMV_BF16                        */
+    int32_t        batch;      /* 0 ..                                           */
+    int32_t        heads;      /* a multiple of the cache's heads                */
+    int32_t        max_pages;
+    int32_t        window;     /* the last `window` tokens are seen; 0: all      */
+    float          scale;      /* finite                                         */
+    float          softcap;    /* >= 0; 0: none                                  */
+    int32_t        reserved;   /* 0                                              */
+} sgemv_attn_args;
+
+/*
+ * sgemv_attn_paged - attention of one new token per sequence over its paged
+ * cache, which already holds that token:
+ *   z(h, i)  = scale * q[b][h] . key(i, h / (heads / kv heads))
+ *              (softcap * tanh(z / softcap) where softcap > 0)
+ *   out[b][h] = sum_i softmax_i(z) value(i),  lse[b][h] = log sum_i exp z
+ * over i in max(0, length - window) .. length - 1.  The lengths are read on
+ * the device: a captured graph serves growing sequences.  The work of a batch
+ * of any lengths is split evenly over the GPU and joined in a fixed order.
+ *   - length 0: out is 0 and lse -infinity.
+ *   - A length below 0 or beyond max_pages * page_size, or a table entry in use
+ *     outside 0 .. pages - 1, makes that sequence's out and lse NaN; nothing out
+ *     of range is read.
+ *   - What stands in a page outside of the seen tokens has no effect, NaN and
+ *     infinities included.
+ * Products of the cache's type (8-bit values as `type`) with fp32 sums;
+ * softmax statistics in fp32; probabilities are rounded to `type` for the
+ * product with the values; one rounding at the end.
+ *   kv->type  `type`, or SGEMV_E4M3
+ *   out       refused where it overlaps an input
+ * EINVAL for NULL, a bad type or value, differing heads or dim, an overlap;
+ * ESIZE for sizes, strides, or too small a workspace
+ * (sgemv_attn_workspace_bytes); EALIGN for pointers.
+ */
+int sgemv_attn_paged(const sgemv_attn_args* a, const sgemv_kv* kv, void* stream);
+
+/* Bytes of workspace of sgemv_attn_paged for up to `batch` sequences; 0 for
+ * sizes out of range. */
+size_t sgemv_attn_workspace_bytes(int32_t batch, int32_t heads, int32_t heads_kv, int32_t dim);
+
+/* Arguments of sgemv_beam_select (host memory, read during the call). */
+typedef struct sgemv_beam_args {
+    const void*    logits;     /* device [batch][beams][vocab] of type            */
+    const float*   scores;     /* device [batch][beams], contiguous               */
+    const uint8_t* finished;   /* device [batch][beams], or NULL                  */
+    int32_t*       tokens;     /* device [batch][choices]                         */
+    int32_t*       parents;    /* device [batch][choices]                         */
+    float*         scores_out; /* device [batch][choices]                         */
+    void*          workspace;  /* device, 256-byte aligned, zero-filled once      */
+    size_t         workspace_bytes;
+    int64_t        ld_batch, ld_beam;   /* of logits, in elements                 */
+    int32_t        type;       /* SGEMV_F16, SGEMV_BF16 or SGEMV_F32              */
+    int32_t        batch;      /* 0 ..                                            */
+    int32_t        beams;      /* 1 .. SGEMV_MAX_BEAMS                            */
+    int32_t        vocab;      /* 1 .. SGEMV_MAX_N                                */
+    int32_t        choices;    /* 1 .. SGEMV_MAX_CHOICES                          */
+    int32_t        end_token;  /* 0 .. vocab - 1 where finished is given          */
+} sgemv_beam_args;
+
+/*
+ * sgemv_beam_select - the best continuations of a batch of beam searches:
+ *   s(w, v) = scores[w] + logits[w][v] - log sum_u exp logits[w][u]
+ * the `choices` largest over beams w and tokens v, largest first, equal ones by
+ * the lowest w, then the largest logit, then the lowest v.  A beam with finished != 0 has one candidate,
+ * end_token, at its own score.  Candidates are those with a finite s: a logit of
+ * -infinity or NaN is none, a beam whose score or whose sum of exponentials is
+ * not finite (or 0) has none.  Where there are fewer than `choices`, the rest
+ * are token -1, parent -1, score -infinity.  s is formed and compared in 64
+ * bits, from fp32 exponentials, and rounded to fp32 at the end.  `parents` is what sgemv_pages_fork takes (as row
+ * batch * beams + parent).
+ * EINVAL for NULL, a bad type or end_token; ESIZE for sizes, strides, too small
+ * a workspace (sgemv_beam_workspace_bytes); EALIGN for pointers.
+ */
+int sgemv_beam_select(const sgemv_beam_args* a, void* stream);
+
+size_t sgemv_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t choices);
+
+/* A batch's pages (host memory): every row lists the pages of its first
+ * ceil(length / page_size) parts, and refs counts the rows' entries of every
+ * page (and whatever else the caller keeps alive); 0 is a free page. */
+typedef struct sgemv_pages_args {
+    const int32_t* table;        /* device [rows][ld_table]                      */
+    const int32_t* lengths;      /* device [rows]                                */
+    const int32_t* refs;         /* device [pages]                               */
+    int32_t*       table_out;    /* device [rows][ld_table_out]; table itself, or
+                                    apart from it; so for the two below          */
+    int32_t*       lengths_out;  /* sgemv_pages_fork only                        */
+    int32_t*       refs_out;
+    const int32_t* parents;      /* fork: device [rows], or NULL: each its own    */
+    const int32_t* grow;         /* fork: device [rows], or NULL: none           */
+    int32_t*       slots;        /* fork: device [rows][max_grow], or NULL        */
+    int32_t*       pairs;        /* device [rows][3] (fork) or [pages][3]
+                                    (compact): source, target, tokens            */
+    int32_t*       count;        /* device [1]: pairs in use; the rest are -1     */
+    int32_t*       status;       /* fork: device [2]                             */
+    void*          workspace;    /* device, 256-byte aligned, zero-filled once   */
+    size_t         workspace_bytes;
+    int64_t        ld_table, ld_table_out;
+    int32_t        rows;         /* 1 .. SGEMV_MAX_ROWS                          */
+    int32_t        max_pages;    /* 1 ..: columns of the tables                  */
+    int32_t        pages;        /* 1 .. 2^24                                    */
+    int32_t        page_size;    /* pages * page_size < 2^31                     */
+    int32_t        max_grow;     /* fork: columns of slots, 0 .. 65536           */
+    int32_t        layers;       /* 0 .. SGEMV_MAX_LAYERS: caches to copy in     */
+} sgemv_pages_args;
+
+/*
+ * sgemv_pages_fork - one step of a batch's pages: rows take over their parents'
+ * pages (beams that change places, one prompt continued several times), rows
+ * end, rows grow.  Row by row in ascending order, as if done one by one:
+ *   1. row r has the first ceil(length / page_size) pages of row parents[r],
+ *      and its length (of the state before the call); a parent outside
+ *      0 .. rows - 1 leaves it empty.  refs gains the new rows' entries and
+ *      loses the old rows'.
+ *   2. a row that grows and whose last page is only partly filled and counted
+ *      more than once gets a page of its own in its place (refs follow); the
+ *      pair (old, new, filled tokens) goes to `pairs`.  Then it gets pages for
+ *      length + grow tokens.  Free pages are taken lowest first, among those
+ *      with a count of 0 after step 1.
+ *   3. slots[r][j], j < grow[r], is the place of new token j, the rest is -1;
+ *      lengths_out has the new lengths; table entries beyond a row's pages
+ *      are -1.
+ *   4. the pairs' tokens are copied in every given cache.
+ * status[1] is the number of rows whose growth is negative, beyond max_grow (with
+ * slots) or beyond max_pages; where that is 0, status[0] is the number of pages
+ * that were missing.  Where either is not 0, step 1 is done and no row grows
+ * (slots -1, count 0).
+ * A row with a length below 0 or beyond max_pages * page_size counts as empty;
+ * entries outside 0 .. pages - 1 are carried along and counted nowhere.
+ *   caches  host array of `layers` caches of one geometry (pages, page_size,
+ *           heads, dim, type, strides), pages and page_size as here; may be
+ *           NULL with layers 0.  More layers: sgemv_pages_copy over the pairs.
+ * EINVAL for NULL, overlaps, caches that differ; ESIZE for sizes, strides, too
+ * small a workspace; EALIGN for pointers.
+ */
+int sgemv_pages_fork(const sgemv_pages_args* a, const sgemv_kv* caches, void* stream);
+
+/*
+ * sgemv_pages_compact - move the pages in use (refs > 0) to the lowest ids: with
+ * U of them, the used pages from U on, ascending, go to the free pages below U,
+ * ascending.  table_out and refs_out follow, `pairs` lists (old, new, page_size)
+ * and the caches are copied as above.  parents, grow, slots, status,
+ * lengths_out are not used.
+ */
+int sgemv_pages_compact(const sgemv_pages_args* a, const sgemv_kv* caches, void* stream);
+
+/*
+ * sgemv_pages_copy - copy the first `tokens` tokens of page `source` to page
+ * `target`, keys and values, in every given cache, for the first min(*count,
+ * max_pairs) rows of pairs (device [max_pairs][3]; count NULL: all).  Rows with
+ * an id outside the cache, or no tokens, are left out; more tokens than
+ * page_size count as page_size.  A page that is the target of one pair should
+ * be neither source nor target of another.
+ */
+int sgemv_pages_copy(const sgemv_kv* caches, int32_t layers, const int32_t* pairs,
+                     const int32_t* count, int32_t max_pairs, void* stream);
+
+/* Bytes of workspace of sgemv_pages_fork and sgemv_pages_compact. */
+size_t sgemv_pages_workspace_bytes(int32_t rows, int32_t max_pages, int32_t pages);
 
 /* Static string for a status code. */
 const char* sgemv_strerror(int status);

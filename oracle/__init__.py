@@ -22,7 +22,8 @@ definition written out in float64:
 
 and the packed weight layout is the byte formula in ``oracle.layout``.
 ``oracle.block`` holds the same kind of definitions for the 4-bit products
-that read every weight, the gated pair and the block norm.
+that read every weight, the gated pair and the block norm, ``oracle.decode``
+those for rotary positions, paged attention, beam selection and pages.
 
 Pins: every function here is checked against values fixed independently of
 it (brute force on tiny inputs, exact rational arithmetic, closed forms and
@@ -32,10 +33,12 @@ from .gemv import (GROUP, active_mask, active_indices, dequantize_columns,
                    gemv_listed, gemv_masked, gemv_dense)
 from .block import (block_norm, gate_function, norm, q4_dequantize, q4_header_fields, q4_pack_spec,
                     q4_product, q4_scale)
+from .decode import (attention, beam_select, paged, pages_compact, pages_fork, rotary, rotary_axes)
 from .layout import pack_spec, unpack_spec, header_fields, read_header
 
 __all__ = ["GROUP", "active_mask", "active_indices", "dequantize_columns",
            "gemv_listed", "gemv_masked", "gemv_dense",
            "pack_spec", "unpack_spec", "header_fields", "read_header",
            "block_norm", "gate_function", "norm", "q4_dequantize", "q4_header_fields", "q4_pack_spec",
-           "q4_product", "q4_scale"]
+           "q4_product", "q4_scale",
+           "attention", "beam_select", "paged", "pages_compact", "pages_fork", "rotary", "rotary_axes"]
