@@ -7,14 +7,14 @@
 // exponentials and its best candidates; the last workgroup of a batch entry to
 // arrive has every beam's normaliser and picks among the parts' candidates.
 //
-// The best n of a part: every lane has its best value, and the n-th best of a
-// wavefront's 64 is found bit by bit with ballots.  n values reach that bound,
-// and so they do the largest of the four wavefronts' bounds; the few dozen
-// values that reach it are ranked, each by counting those above it.  Where
-// they are too many (sorted or equal logits), the n-th best of all 256 threads
-// is taken instead, which the values of n threads only can reach.  The same
-// bound over the parts' best values leaves n parts, and of the part that is
-// r-th best by its first value only the first n - r can be among the best n.
+// The best n of a part: every lane has its largest value, and the n-th largest
+// of a wavefront's 64 is found bit by bit with ballots.  n values reach that
+// bound, and so they do the largest of the four wavefronts' bounds; the few
+// dozen values that reach it are ranked, each by counting those above it.
+// Where equal values make them too many, the threads' best are told apart by
+// their places, and the n-th best of those is a bound that only the values of
+// n threads can reach.  The same over the parts' best values: of the part that
+// is r-th by its first value only the first n - r can be among the best n.
 // Within a beam the logits' order is that of s, and equal values go by their
 // place, so every key is unique and the answer does not depend on timing.
 //
@@ -34,6 +34,7 @@ typedef uint32_t uint4_w __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kThreads = 256;
 constexpr int kMaxBatch = 2048;        // entries of one launch
+constexpr int kMostTied = 6 * kThreads; // a part's values to be ranked, before their places tell them apart
 constexpr int kCounterStep = 16;       // words between arrival counters
 constexpr size_t kCounterBytes = (size_t)kMaxBatch * kCounterStep * 4;
 
@@ -47,7 +48,6 @@ struct Args {
     uint64_t* parts_out;          // per beam and part: choices keys, then maximum and sum
     int64_t ld_batch, ld_beam;    // elements
     int32_t beams, vocab, choices, parts, slice, end_token;
-    int32_t cap, lists;           // candidates and lists that LDS has room for
 };
 
 // Bits of a widened value that are always the same.
@@ -109,20 +109,48 @@ __device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
     }
 }
 
-template <class V>
-__device__ __forceinline__ V wave_max(V v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const V o = __shfl_xor(v, d);
-        v = v > o ? v : o;
-    }
-    return v;
+// Sums and maxima over 16 lanes (by rotations) and over all 64, by moves within
+// the vector unit.
+template <int N>
+__device__ __forceinline__ float turned(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xF, 0xF, false));
+}
+template <int N>
+__device__ __forceinline__ double turned(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x120 + N, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x120 + N, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, turned<1>(v));
+    v = fmaxf(v, turned<2>(v));
+    v = fmaxf(v, turned<4>(v));
+    return fmaxf(v, turned<8>(v));
 }
 template <class V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+__device__ __forceinline__ V row_sum(V v) {
+    v += turned<1>(v);
+    v += turned<2>(v);
+    v += turned<4>(v);
+    return v + turned<8>(v);
+}
+// (A bit cast of a vector's element itself reads element 0: these take it as a number.)
+__device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
+__device__ __forceinline__ uint32_t as_u32(float v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ float wave_max(float v) {
+    v = row_max(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = fmaxf(as_float(x[0]), as_float(x[1]));
+    const auto y = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return fmaxf(as_float(y[0]), as_float(y[1]));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v = row_sum(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = as_float(x[0]) + as_float(x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return as_float(y[0]) + as_float(y[1]);
 }
 
 // One beam's candidate: beam, logit and token in one number, larger for the one to prefer among equal s.
@@ -132,20 +160,17 @@ __device__ __forceinline__ uint64_t place_of(int beam, uint64_t key) {
 
 __device__ __forceinline__ int lanes(bool v) { return __popcll(__ballot(v)); }
 
-// The n-th best of the wavefront's 64 keys (value above place; 0 is none), or 0
-// where fewer than n are there.
-template <int TYPE>
-__device__ __forceinline__ uint64_t nth_of_wave(uint64_t key, int n) {
-    const uint32_t value = (uint32_t)(key >> 32), place = (uint32_t)key;
-    uint32_t t = 0, p = 0;
-    for (int bit = 31 - kFixed<TYPE>; bit >= 0; --bit)
-        if (lanes(value >= (t | 1u << bit)) >= n) t |= 1u << bit;
-    if (t == 0) return 0;
-    const int need = n - lanes(value > t);
-    if (lanes(value == t) > need)
-        for (int bit = 31; bit >= 0; --bit)
-            if (lanes(value == t && place >= (p | 1u << bit)) >= need) p |= 1u << bit;
-    return (uint64_t)t << 32 | p;
+// The n-th largest of the wavefront's 64 keys, or 0 where fewer than n are
+// above it.
+template <int BITS>
+__device__ __forceinline__ uint32_t nth_of_wave(uint32_t key, int n) {
+    uint32_t t = 0;
+#pragma unroll 4
+    for (int bit = BITS - 1; bit >= 0; --bit) {
+        const uint32_t trial = t | 1u << bit;
+        if (lanes(key >= trial) >= n) t = trial;
+    }
+    return t;
 }
 
 struct Candidate {
@@ -155,14 +180,69 @@ __device__ __forceinline__ bool above(const Candidate& a, const Candidate& b) {
     return a.s > b.s || (a.s == b.s && a.place > b.place);
 }
 
-// RUNS runs of eight values a thread.
-template <int TYPE, int RUNS>
-__global__ __launch_bounds__(kThreads) void k_beam(Args a) {
+// Rank of item i of a list of `count` in LDS, counted by `per` neighbouring
+// threads together (a power of two up to 64).
+template <class V, class F>
+__device__ __forceinline__ int rank_of(const V* list, int count, const V& item, int per, F above_it) {
+    int rank = 0;
+#pragma unroll 8
+    for (int k = (int)threadIdx.x & (per - 1); k < count; k += per) rank += above_it(list[k], item);
+    for (int d = 1; d < per; d <<= 1) rank += __shfl_xor(rank, d);
+    return rank;
+}
+// Threads that count together for each of `count` items.
+__device__ __forceinline__ int threads_per(int count) {
+    int per = 1;
+    while (per < 64 && count * per * 2 <= kThreads) per *= 2;
+    return per;
+}
+
+// Drops items that cannot be among the n best of a list of up to PER * kThreads
+// in LDS: those below the n-th largest key, found bit by bit.  Ranking is
+// quadratic, so it pays from some hundred items on.  Returns the new count.
+template <int PER, class V, class F>
+__device__ __forceinline__ int tighten(V* list, int count, int n, uint32_t* counts, uint32_t* left, F key) {
+    if (count <= 2 * n + 96) return count;
+    const int tid = threadIdx.x;
+    V mine[PER];
+    uint32_t k[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        k[i] = 0;
+        if (tid + i * kThreads < count) {
+            mine[i] = list[tid + i * kThreads];
+            k[i] = key(mine[i]);
+        }
+    }
+    if (tid < 32) counts[tid] = 0;
+    if (tid == 32) *left = 0;
+    __syncthreads();
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t trial = t | 1u << bit;
+        int here = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i * kThreads < count) here += lanes(k[i] >= trial);
+        if ((tid & 63) == 0 && here) atomicAdd(&counts[bit], (uint32_t)here);
+        __syncthreads();
+        if (counts[bit] >= (uint32_t)n) t = trial;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (tid + i * kThreads < count && k[i] >= t) list[atomicAdd(left, 1u)] = mine[i];
+    __syncthreads();
+    return (int)*left;
+}
+
+// RUNS runs of eight values a thread, at most N choices.
+template <int TYPE, int RUNS, int N>
+__global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
     extern __shared__ uint64_t lds[];
-    __shared__ float part_m[kThreads / 64], part_s[kThreads / 64];
+    __shared__ float part_m[kThreads / 64], part_s[kThreads / 64], part_t[kThreads / 64];
     __shared__ double offset[SGEMV_MAX_BEAMS];
-    __shared__ uint32_t left;
-    __shared__ uint64_t wave_bound[kThreads / 64];
+    __shared__ uint32_t left, counts[32], wave_bound[kThreads / 64], order[N];
+    __shared__ uint64_t part_bound;
     __shared__ Candidate bound;
     constexpr int ES = TYPE == SGEMV_F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.choices;
@@ -170,12 +250,13 @@ __global__ __launch_bounds__(kThreads) void k_beam(Args a) {
     const int entry = (int)(blockIdx.x / a.parts) / a.beams;
     const int record = n + 1;
     uint64_t* mine = a.parts_out + (int64_t)blockIdx.x * record;
+    const auto order_of = [](uint64_t x, uint64_t y) { return x > y; };
 
     const bool done = a.finished && a.finished[entry * a.beams + beam];
     if (!done) {
         const uint8_t* row = a.logits + (entry * a.ld_batch + beam * a.ld_beam) * ES;
         const int first = part * a.slice, end = first + a.slice < a.vocab ? first + a.slice : a.vocab;
-        float v[RUNS][8];
+        float v[RUNS][8], run_top[RUNS];
 #pragma unroll
         for (int r = 0; r < RUNS; ++r) {
             const int at = first + (r * kThreads + tid) * 8;
@@ -191,84 +272,95 @@ __global__ __launch_bounds__(kThreads) void k_beam(Args a) {
             }
         }
         float top = -INFINITY;
-        int top_at = 0;   // the first of a thread's values that is its largest
 #pragma unroll
-        for (int r = 0; r < RUNS; ++r)
+        for (int r = 0; r < RUNS; ++r) {
+            run_top[r] = v[r][0];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (v[r][j] > top) {
-                    top = v[r][j];
-                    top_at = first + (r * kThreads + tid) * 8 + j;
-                }
+            for (int j = 1; j < 8; ++j) run_top[r] = fmaxf(run_top[r], v[r][j]);
+            top = fmaxf(top, run_top[r]);
+        }
         const float wm = wave_max(top);
-        // a thread's best, with the place turned round so that the lowest wins among equals
-        const uint32_t top_key = key_of<TYPE>(top);
-        const uint64_t best = top_key ? (uint64_t)top_key << 32 | ~(uint32_t)top_at : 0ull;
-        const uint64_t nth = nth_of_wave<TYPE>(best, n);
+        const uint32_t nth = nth_of_wave<32 - kFixed<TYPE>>(key_of<TYPE>(top), n);
         if (lane == 0) {
             part_m[wave] = wm;
-            wave_bound[wave] = nth;
+            part_t[wave] = nth ? value_of<TYPE>(nth) : -3.4028234664e38f;   // no bound: any finite value
         }
-        if (tid == 0) left = 0;
+        if (tid == 0) {
+            left = 0;
+            part_bound = 0;
+        }
         __syncthreads();
-        float m = part_m[0];
-        uint64_t least = wave_bound[0];
+        float m = part_m[0], least = part_t[0];
 #pragma unroll
         for (int w = 1; w < kThreads / 64; ++w) {
             m = fmaxf(m, part_m[w]);
-            least = least > wave_bound[w] ? least : wave_bound[w];
+            least = fmaxf(least, part_t[w]);
         }
         const float from = m == -INFINITY ? 0.0f : m;
         float sum = 0.0f;
-        int reach = 0;
 #pragma unroll
         for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = v[r][j] - from;
-                // log2(e) in two parts: what its rounding takes from far logits would add up
-                const float e = __builtin_amdgcn_exp2f(fmaf(d, 1.44269502e+0f, d * 1.92596299e-8f));
-                if (v[r][j] == v[r][j]) sum += e;
-                const uint64_t key = (uint64_t)key_of<TYPE>(v[r][j]) << 32 | ~(uint32_t)(first + (r * kThreads + tid) * 8 + j);
-                reach += key >> 32 && key >= least;
-            }
+            for (int j = 0; j < 8; ++j) sum += __builtin_amdgcn_exp2f((v[r][j] - from) * 1.44269504e+0f);
         sum = wave_sum(sum);
-        reach = wave_sum(reach);
-        if (lane == 0) {
-            part_s[wave] = sum;
-            if (reach) atomicAdd(&left, (uint32_t)reach);
+        if (sum != sum) {   // NaN among the logits is left out; an infinity stays
+            sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (v[r][j] == v[r][j]) sum += __builtin_amdgcn_exp2f((v[r][j] - from) * 1.44269504e+0f);
+            sum = wave_sum(sum);
+        }
+        if (lane == 0) part_s[wave] = sum;
+        const auto place = [&](int r, int j) { return ~(uint32_t)(first + (r * kThreads + tid) * 8 + j); };
+        const uint32_t room = kMostTied;
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) {
+            if (!(run_top[r] >= least)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (v[r][j] >= least) {
+                    const uint32_t at = atomicAdd(&left, 1u);
+                    if (at < room) lds[at] = (uint64_t)key_of<TYPE>(v[r][j]) << 32 | place(r, j);
+                }
         }
         __syncthreads();
-        const bool many = left > (uint32_t)(2 * a.cap);
-        __syncthreads();
-        if (many) {
-            if (tid == 0) wave_bound[0] = 0;
-            lds[tid] = best;
+        if (left > room) {   // the same in every thread
             __syncthreads();
-            int rank = 0;
-            for (int i = 0; i < kThreads; ++i) rank += lds[i] > best;
-            if (rank == n - 1 && best) wave_bound[0] = best;
-            __syncthreads();
-            least = wave_bound[0];
-        }
-        if (tid == 0) left = 0;
-        __syncthreads();
-        if (best && best >= least) {
+            uint64_t best = 0;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint64_t key = (uint64_t)key_of<TYPE>(v[r][j]) << 32 | ~(uint32_t)(first + (r * kThreads + tid) * 8 + j);
-                    if (key >> 32 && key >= least) lds[atomicAdd(&left, 1u)] = key;
+                    const uint64_t k = key_of<TYPE>(v[r][j]), key = k << 32 | place(r, j);
+                    if (k && key > best) best = key;
                 }
+            lds[tid] = best;
+            if (tid == 0) left = 0;
+            __syncthreads();
+            const int rank = rank_of(lds, kThreads, best, 1, order_of);
+            if (rank == n - 1 && best) part_bound = best;
+            __syncthreads();
+            const uint64_t bound_key = part_bound;
+            if (best && best >= bound_key) {
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint64_t k = key_of<TYPE>(v[r][j]), key = k << 32 | place(r, j);
+                        if (k && key >= bound_key) lds[atomicAdd(&left, 1u)] = key;
+                    }
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        const int count = (int)left;
-        for (int i = tid; i < count; i += kThreads) {
+        constexpr int kMost = N * RUNS * 8 > kMostTied ? N * RUNS * 8 : kMostTied;
+        const int count = tighten<kMost / kThreads>(lds, (int)left, n, counts, &left, [](uint64_t k) { return (uint32_t)(k >> 32); });
+        const int per = threads_per(count);
+        for (int i = tid / per; i < count; i += kThreads / per) {
             const uint64_t key = lds[i];
-            int above_it = 0;
-            for (int k = 0; k < count; ++k) above_it += lds[k] > key;
-            if (above_it < n) publish(mine + above_it, key);
+            const int rank = rank_of(lds, count, key, per, order_of);
+            if (rank < n && (tid & (per - 1)) == 0) publish(mine + rank, key);
         }
         if (tid >= count && tid < n) publish(mine + tid, 0ull);
         if (tid == 0) {
@@ -292,109 +384,110 @@ __global__ __launch_bounds__(kThreads) void k_beam(Args a) {
     if (!last) return;
 
     const uint64_t* records = a.parts_out + (int64_t)entry * lists * record;
-    for (int w = wave; w < a.beams; w += kThreads / 64) {
-        const float score = a.scores[entry * a.beams + w];
-        double off = (double)score;
-        if (!(a.finished && a.finished[entry * a.beams + w])) {
-            float m = -INFINITY;
-            for (int p = lane; p < a.parts; p += 64)
-                m = fmaxf(m, __builtin_bit_cast(float, (uint32_t)(fetch(records + (int64_t)(w * a.parts + p) * record + n) >> 32)));
-            m = wave_max(m);
-            double s = 0.0;
-            for (int p = lane; p < a.parts; p += 64) {
-                const uint64_t ms = fetch(records + (int64_t)(w * a.parts + p) * record + n);
-                const float pm = __builtin_bit_cast(float, (uint32_t)(ms >> 32)), ps = __builtin_bit_cast(float, (uint32_t)ms);
-                if (pm > -INFINITY) s += (double)ps * exp((double)pm - (double)m);
+    const auto ended = [&](int w) { return a.finished && a.finished[entry * a.beams + w]; };
+    // the parts' sums, and at the same time each thread's first list's best
+    const uint64_t first_key = tid < lists ? fetch(records + (int64_t)tid * record) : 0;
+    for (int i = tid; i < lists; i += kThreads) lds[i] = fetch(records + (int64_t)i * record + n);
+    if (tid == 0) left = 0;
+    __syncthreads();
+    for (int w0 = 0; w0 < a.beams; w0 += kThreads / 16) {   // 16 lanes a beam
+        const int w = w0 + tid / 16;
+        if (w < a.beams) {
+            double off = (double)a.scores[entry * a.beams + w];
+            if (!ended(w)) {
+                float m = -INFINITY;
+                for (int p = tid & 15; p < a.parts; p += 16) m = fmaxf(m, __builtin_bit_cast(float, (uint32_t)(lds[w * a.parts + p] >> 32)));
+                m = row_max(m);
+                double s = 0.0;
+                for (int p = tid & 15; p < a.parts; p += 16) {
+                    const uint64_t ms = lds[w * a.parts + p];
+                    const float pm = __builtin_bit_cast(float, (uint32_t)(ms >> 32)), ps = __builtin_bit_cast(float, (uint32_t)ms);
+                    if (pm > -INFINITY) s += (double)(ps * __builtin_amdgcn_exp2f((pm - m) * 1.44269504e+0f));
+                }
+                s = row_sum(s);
+                off -= (double)m + log(s);   // not finite where no logit or an infinite one is there
             }
-            s = wave_sum(s);
-            off = (double)score - ((double)m + log(s));   // not finite where no logit or an infinite one is there
+            if ((tid & 15) == 0) offset[w] = off;
         }
-        if (lane == 0) offset[w] = off;
-    }
-    if (tid == 0) {
-        left = 0;
-        bound = Candidate{0, 0};
     }
     __syncthreads();
 
-    Candidate* found = reinterpret_cast<Candidate*>(lds);                       // cap of them
-    Candidate* head = found + a.cap;                                            // the parts' first values
-    uint32_t* head_list = reinterpret_cast<uint32_t*>(head + a.lists);
-    const auto candidate = [&](int list, int i) {
+    Candidate* found = reinterpret_cast<Candidate*>(lds);   // lists by their best, later the values that may be chosen
+    uint32_t* found_list = reinterpret_cast<uint32_t*>(found + lists);
+    const auto candidate = [&](int list, int i, uint64_t key) {
         const int w = list / a.parts;
         Candidate c = {0, 0};
         const double off = offset[w];
-        if (!(off - off == 0.0)) return c;                                      // not finite: no candidates
-        if (a.finished && a.finished[entry * a.beams + w]) {
+        if (!(off - off == 0.0)) return c;                  // not finite: no candidates
+        if (ended(w)) {
             if (i == 0 && list == w * a.parts) c = Candidate{key_of(off), (uint64_t)(63 - w) << 52 | (0xFFFFFu - (uint32_t)a.end_token)};
             return c;
         }
-        const uint64_t key = fetch(records + (int64_t)list * record + i);
         if (key) c = Candidate{key_of((double)value_of<TYPE>((uint32_t)(key >> 32)) + off), place_of(w, key)};
         return c;
     };
-    // a bound on the parts' first values, and those that reach it
-    Candidate best = {0, 0};
-    for (int i = tid; i < lists; i += kThreads) {
-        const Candidate c = candidate(i, 0);
-        if (above(c, best)) best = c;
+    const auto kth = [&](int list, int i) { return fetch(records + (int64_t)list * record + i); };
+    // a bound that n of the lists' best reach: the n-th of a wavefront's threads
+    const Candidate first = tid < lists ? candidate(tid, 0, first_key) : Candidate{0, 0};
+    uint64_t best = first.s;
+    for (int i = tid + kThreads; i < lists; i += kThreads) {
+        const uint64_t c = candidate(i, 0, kth(i, 0)).s;
+        best = best > c ? best : c;
     }
-    found[tid] = best;
+    const uint32_t nth = nth_of_wave<32>((uint32_t)(best >> 32), n);
+    if (lane == 0) wave_bound[wave] = nth;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < kThreads; ++i) rank += above(found[i], best);
-    if (rank == n - 1 && best.s) bound = best;
-    __syncthreads();
-    Candidate least = bound;
-    for (int i = tid; i < lists; i += kThreads) {
-        if (!(rank < n && best.s)) break;
-        const Candidate c = candidate(i, 0);
-        if (c.s && !above(least, c)) {
+    uint32_t reach = wave_bound[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w) reach = reach > wave_bound[w] ? reach : wave_bound[w];
+    const auto enlist = [&](int i, const Candidate& c) {
+        if (c.s && (uint32_t)(c.s >> 32) >= reach) {
             const uint32_t at = atomicAdd(&left, 1u);
-            head[at] = c;
-            head_list[at] = (uint32_t)i;
+            found[at] = c;
+            found_list[at] = (uint32_t)i;
         }
-    }
+    };
+    enlist(tid, first);
+    for (int i = tid + kThreads; i < lists; i += kThreads) enlist(i, candidate(i, 0, kth(i, 0)));
+    if (tid == 0) bound = Candidate{0, 0};
     __syncthreads();
-    const int heads = (int)left;
-    __syncthreads();
-    // their order: of the r-th, the first n - r values can be among the best n
-    uint32_t* order = reinterpret_cast<uint32_t*>(found);
-    for (int i = tid; i < heads; i += kThreads) {
-        const Candidate c = head[i];
-        int r = 0;
-        for (int k = 0; k < heads; ++k) r += above(head[k], c);
-        if (r < n) order[r] = head_list[i];
+    // their order
+    const int holders = (int)left, per_holder = threads_per(holders);
+    for (int i = tid / per_holder; i < holders; i += kThreads / per_holder) {
+        const Candidate c = found[i];
+        const int r = rank_of(found, holders, c, per_holder, above);
+        if (r < n) order[r] = found_list[i];
         if (r == n - 1) bound = c;
     }
+    __syncthreads();
+    const int used = holders < n ? holders : n;
+    const Candidate least = bound;
+    // pair (r, j): value j of the r-th list
+    constexpr int kPairs = (N * N + kThreads - 1) / kThreads;
     if (tid == 0) left = 0;
     __syncthreads();
-    const int used = heads < n ? heads : n;
-    least = bound;
-    // pair (r, j): value j of the r-th part.  A thread's parts are read before found, which order shares, is written
-    constexpr int kPairs = (SGEMV_MAX_CHOICES * SGEMV_MAX_CHOICES + kThreads - 1) / kThreads;
-    uint32_t list[kPairs];
+    uint64_t key[kPairs];
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-        const int x = tid + i * kThreads;
-        list[i] = x < used * n ? order[x / n] : 0;
+        const int x = tid + i * kThreads, r = x / n, j = x - r * n;
+        key[i] = r < used && r + j < n ? kth((int)order[r], j) : 0;
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
         const int x = tid + i * kThreads, r = x / n, j = x - r * n;
         if (r >= used || r + j >= n) continue;
-        const Candidate c = candidate((int)list[i], j);
+        const Candidate c = candidate((int)order[r], j, key[i]);
         if (c.s && !above(least, c)) found[atomicAdd(&left, 1u)] = c;
     }
     __syncthreads();
-    const int count = (int)left;
+    constexpr int kMostFound = (N * (N + 1) / 2 + kThreads - 1) / kThreads;
+    const int count = tighten<kMostFound>(found, (int)left, n, counts, &left, [](const Candidate& c) { return (uint32_t)(c.s >> 32); });
+    const int per = threads_per(count);
     const int64_t out = (int64_t)entry * n;
-    for (int i = tid; i < count; i += kThreads) {
+    for (int i = tid / per; i < count; i += kThreads / per) {
         const Candidate c = found[i];
-        int r = 0;
-        for (int k = 0; k < count; ++k) r += above(found[k], c);
-        if (r < n) {
+        const int r = rank_of(found, count, c, per, above);
+        if (r < n && (tid & (per - 1)) == 0) {
             a.tokens[out + r] = (int32_t)(0xFFFFFu - (uint32_t)(c.place & 0xFFFFFu));
             a.parents[out + r] = 63 - (int32_t)(c.place >> 52);
             a.scores_out[out + r] = (float)score_of(c.s);
@@ -408,30 +501,37 @@ __global__ __launch_bounds__(kThreads) void k_beam(Args a) {
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+int64_t parts_of(int vocab, int runs) { return (vocab + runs * kThreads * 8 - 1) / (runs * kThreads * 8); }
+
 // How a beam's vocabulary is cut: parts of RUNS * 2048 values at most, equal
 // and whole runs of eight.
 struct Cut {
     int runs, parts, slice;
 };
-Cut cut_of(int64_t rows, int vocab) {
+Cut cut_of(int64_t rows, int beams, int vocab) {
     Cut c;
-    const int64_t large = (vocab + 8191) / 8192;
-    c.runs = rows * large >= 512 ? 4 : 1;
-    const int most = c.runs * kThreads * 8;
-    c.parts = (vocab + most - 1) / most;
+    for (c.runs = 1; c.runs < 4; c.runs *= 2) {
+        const int64_t parts = parts_of(vocab, c.runs);
+        if (rows * parts <= 512 && beams * parts <= kThreads) break;
+    }
+    c.parts = (int)parts_of(vocab, c.runs);
     c.slice = ((vocab + c.parts - 1) / c.parts + 7) / 8 * 8;
     c.parts = (vocab + c.slice - 1) / c.slice;
     return c;
 }
 
 typedef void (*Kernel)(Args);
+template <int TYPE, int N>
+Kernel pick_runs(int runs) {
+    return runs == 4 ? k_beam<TYPE, 4, N> : runs == 2 ? k_beam<TYPE, 2, N> : k_beam<TYPE, 1, N>;
+}
 template <int TYPE>
-Kernel pick(int runs) {
-    return runs == 4 ? k_beam<TYPE, 4> : k_beam<TYPE, 1>;
+Kernel pick(int runs, int choices) {
+    return choices <= 16 ? pick_runs<TYPE, 16>(runs) : pick_runs<TYPE, SGEMV_MAX_CHOICES>(runs);
 }
 
 bool sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t choices) {
-    return batch >= 0 && beams >= 1 && beams <= SGEMV_MAX_BEAMS && vocab >= 1 && vocab <= SGEMV_MAX_N && choices >= 1 &&
+    return batch >= 0 && beams >= 1 && beams <= SGEMV_MAX_BEAMS && vocab >= 1 && vocab <= SGEMV_MAX_VOCAB && choices >= 1 &&
            choices <= SGEMV_MAX_CHOICES;
 }
 
@@ -439,12 +539,11 @@ bool sizes_ok(int32_t batch, int32_t beams, int32_t vocab, int32_t choices) {
 
 extern "C" size_t sgemv_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t choices) {
     if (!sizes_ok(batch, beams, vocab, choices)) return 0;
-    // launches of at most kMaxBatch entries; the finest cut of any batch up to this one
+    // launches of at most kMaxBatch entries; the last may have few and so a finer cut
     const int64_t entries = batch < kMaxBatch ? batch : kMaxBatch;
-    const int64_t fine = (vocab + kThreads * 8 - 1) / (kThreads * 8), coarse = (vocab + 8191) / 8192;
-    int64_t records = entries * beams * coarse;
-    const int64_t few = 511 < entries * beams * coarse ? 511 : entries * beams * coarse;   // rows * coarse of a fine cut
-    if (few / coarse * fine > records) records = few / coarse * fine;
+    int64_t records = entries * beams * parts_of(vocab, 4);
+    const int64_t finer = 512 < entries * beams * parts_of(vocab, 1) ? 512 : entries * beams * parts_of(vocab, 1);
+    if (finer > records) records = finer;
     return kCounterBytes + (size_t)records * (choices + 1) * 8;
 }
 
@@ -486,7 +585,7 @@ extern "C" int sgemv_beam_select(const sgemv_beam_args* args, void* stream) {
     a.end_token = p.end_token;
     for (int64_t b = 0; b < p.batch; b += kMaxBatch) {
         const int64_t entries = p.batch - b < kMaxBatch ? p.batch - b : kMaxBatch;
-        const Cut cut = cut_of(entries * p.beams, p.vocab);
+        const Cut cut = cut_of(entries * p.beams, p.beams, p.vocab);
         a.logits = static_cast<const uint8_t*>(p.logits) + b * p.ld_batch * size;
         a.scores = p.scores + b * p.beams;
         a.finished = p.finished ? p.finished + b * p.beams : nullptr;
@@ -496,13 +595,15 @@ extern "C" int sgemv_beam_select(const sgemv_beam_args* args, void* stream) {
         a.parts = cut.parts;
         a.slice = cut.slice;
         const int lists = p.beams * cut.parts, n = p.choices;
-        a.cap = n * (n + 1) / 2 > kThreads ? n * (n + 1) / 2 : kThreads;
-        if (a.cap * 2 < n * cut.runs * 8) a.cap = n * cut.runs * 4;   // the values of n threads, half as large
-        a.lists = n * ((lists + kThreads - 1) / kThreads);
-        const size_t shared = (size_t)a.cap * 16 + (size_t)a.lists * 20;
-        const Kernel kernel = p.type == SGEMV_F16    ? pick<SGEMV_F16>(cut.runs)
-                              : p.type == SGEMV_BF16 ? pick<SGEMV_BF16>(cut.runs)
-                                                     : pick<SGEMV_F32>(cut.runs);
+        // in LDS: the values of n threads or kMostTied of them (8 bytes); the lists by their best (20); the values that may
+        // be chosen (16)
+        const int cap = n * cut.runs * 8 > kMostTied ? n * cut.runs * 8 : kMostTied;
+        size_t shared = (size_t)cap * 8;
+        if (shared < (size_t)lists * 20) shared = (size_t)lists * 20;
+        if (shared < (size_t)n * (n + 1) / 2 * 16) shared = (size_t)n * (n + 1) / 2 * 16;
+        const Kernel kernel = p.type == SGEMV_F16    ? pick<SGEMV_F16>(cut.runs, n)
+                              : p.type == SGEMV_BF16 ? pick<SGEMV_BF16>(cut.runs, n)
+                                                     : pick<SGEMV_F32>(cut.runs, n);
         void* kargs[] = {&a};
         const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)(entries * lists)),
                                              dim3(kThreads), kargs, shared, static_cast<hipStream_t>(stream));

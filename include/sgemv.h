@@ -614,6 +614,7 @@ int sgemv_block_norm(const sgemv_norm* a, void* stream);
 #define SGEMV_MAX_AXES    4
 #define SGEMV_MAX_BEAMS   32
 #define SGEMV_MAX_CHOICES 64
+#define SGEMV_MAX_VOCAB   (1 << 19)
 #define SGEMV_MAX_LAYERS  128
 #define SGEMV_MAX_ROWS    8192
 
@@ -755,7 +756,7 @@ typedef struct sgemv_beam_args {
     int32_t        type;       /* SGEMV_F16, SGEMV_BF16 or SGEMV_F32              */
     int32_t        batch;      /* 0 ..                                            */
     int32_t        beams;      /* 1 .. SGEMV_MAX_BEAMS                            */
-    int32_t        vocab;      /* 1 .. SGEMV_MAX_N                                */
+    int32_t        vocab;      /* 1 .. SGEMV_MAX_VOCAB                            */
     int32_t        choices;    /* 1 .. SGEMV_MAX_CHOICES                          */
     int32_t        end_token;  /* 0 .. vocab - 1 where finished is given          */
 } sgemv_beam_args;

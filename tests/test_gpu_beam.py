@@ -82,9 +82,12 @@ def test_batches(B):
 
 
 def test_large_vocabulary_and_the_coarse_cut():
-    check(*problem(1, 1, 2, 1 << 20, "bf16"), 16)
+    check(*problem(1, 1, 2, 1 << 19, "bf16"), 16)
     check(*problem(2, 40, 8, 16500, "f16"), 16)
     check(*problem(3, 40, 8, 16500, "f32"), 64)
+    check(*problem(4, 1, 32, 1 << 18, "f32"), 64)
+    check(*problem(5, 1, 8, 100003, "bf16"), 16)
+    check(*problem(6, 1, 3, 40000, "f16"), 6)
 
 
 def test_more_entries_than_a_launch_holds():
