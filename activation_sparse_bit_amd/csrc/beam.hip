@@ -7,14 +7,14 @@
 // exponentials and its best candidates; the last workgroup of a batch entry to
 // arrive has every beam's normaliser and picks among the parts' candidates.
 //
-// The best n of a part: every lane has its largest value, and the n-th largest
-// of a wavefront's 64 is found bit by bit with ballots.  n values reach that
-// bound, and so they do the largest of the four wavefronts' bounds; the few
-// dozen values that reach it are ranked, each by counting those above it.
-// Where equal values make them too many, the threads' best are told apart by
-// their places, and the n-th best of those is a bound that only the values of
-// n threads can reach.  The same over the parts' best values: of the part that
-// is r-th by its first value only the first n - r can be among the best n.
+// The best n of a part: every lane has its largest value, and the k-th largest
+// of a wavefront's 64 is found bit by bit with ballots.  With k = n / 4, n values
+// reach the smallest of the four wavefronts' bounds; the few dozen values that
+// do are ranked, each by counting those above it.  Where equal values make them
+// too many, the threads' best are told apart by their places, and the n-th best
+// of those is a bound that only the values of n threads can reach.  Much the
+// same picks the parts that matter by their best values, and of the part that is
+// r-th by its best only the first n - r values can be among the best n.
 // Within a beam the logits' order is that of s, and equal values go by their
 // place, so every key is unique and the answer does not depend on timing.
 //
@@ -35,6 +35,7 @@ typedef uint32_t uint4_w __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kThreads = 256;
 constexpr int kMaxBatch = 2048;        // entries of one launch
 constexpr int kMostTied = 6 * kThreads; // a part's values to be ranked, before their places tell them apart
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kCounterStep = 16;       // words between arrival counters
 constexpr size_t kCounterBytes = (size_t)kMaxBatch * kCounterStep * 4;
 
@@ -90,24 +91,23 @@ __device__ __forceinline__ float widen(uint32_t bits) {
     return __builtin_bit_cast(float, bits);
 }
 
+// Eight values from any element on.
 template <int TYPE>
-__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
-    if (TYPE == SGEMV_F32) {
-        const uint4_t a = *reinterpret_cast<const uint4_w*>(p), b = *reinterpret_cast<const uint4_w*>(p + 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = widen<TYPE>(a[i]);
-            v[4 + i] = widen<TYPE>(b[i]);
-        }
-    } else {
-        const uint4_t a = *reinterpret_cast<const uint4_h*>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = widen<TYPE>(a[i] & 0xFFFFu);
-            v[2 * i + 1] = widen<TYPE>(a[i] >> 16);
+struct Run {
+    uint4_t a, b;
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        if constexpr (TYPE == SGEMV_F32) {
+            a = *reinterpret_cast<const uint4_w*>(p);
+            b = *reinterpret_cast<const uint4_w*>(p + 16);
+        } else {
+            a = *reinterpret_cast<const uint4_h*>(p);
         }
     }
-}
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (TYPE == SGEMV_F32) return widen<TYPE>(j < 4 ? a[j] : b[j - 4]);
+        else return widen<TYPE>(j & 1 ? a[j >> 1] >> 16 : a[j >> 1] & 0xFFFFu);
+    }
+};
 
 // Sums and maxima over 16 lanes (by rotations) and over all 64, by moves within
 // the vector unit.
@@ -153,6 +153,13 @@ __device__ __forceinline__ float wave_sum(float v) {
     return as_float(y[0]) + as_float(y[1]);
 }
 
+// The largest of three; where one is NaN, possibly NaN (fmaxf would take two more instructions for that).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // One beam's candidate: beam, logit and token in one number, larger for the one to prefer among equal s.
 __device__ __forceinline__ uint64_t place_of(int beam, uint64_t key) {
     return (uint64_t)(63 - beam) << 52 | (key >> 32) << 20 | (0xFFFFFu - (~(uint32_t)key & 0xFFFFFu));
@@ -190,6 +197,25 @@ __device__ __forceinline__ int rank_of(const V* list, int count, const V& item, 
     for (int d = 1; d < per; d <<= 1) rank += __shfl_xor(rank, d);
     return rank;
 }
+// The same for candidates: by the upper half of s, and by all of it where another has the same.
+__device__ __forceinline__ int rank_of(const Candidate* list, int count, const Candidate& item, int per) {
+    const uint32_t mine = (uint32_t)(item.s >> 32);
+    const uint32_t* upper = reinterpret_cast<const uint32_t*>(list) + 1;
+    int rank = 0, same = 0;
+#pragma unroll 8
+    for (int k = (int)threadIdx.x & (per - 1); k < count; k += per) {
+        const uint32_t other = upper[4 * k];
+        rank += other > mine;
+        same += other == mine;
+    }
+    for (int d = 1; d < per; d <<= 1) {
+        rank += __shfl_xor(rank, d);
+        same += __shfl_xor(same, d);
+    }
+    if (same > 1)   // the same in all threads of an item
+        rank = rank_of(list, count, item, per, above);
+    return rank;
+}
 // Threads that count together for each of `count` items.
 __device__ __forceinline__ int threads_per(int count) {
     int per = 1;
@@ -199,10 +225,10 @@ __device__ __forceinline__ int threads_per(int count) {
 
 // Drops items that cannot be among the n best of a list of up to PER * kThreads
 // in LDS: those below the n-th largest key, found bit by bit.  Ranking is
-// quadratic, so it pays from some hundred items on.  Returns the new count.
+// quadratic, so it pays from some dozen items on.  Returns the new count.
 template <int PER, class V, class F>
 __device__ __forceinline__ int tighten(V* list, int count, int n, uint32_t* counts, uint32_t* left, F key) {
-    if (count <= 2 * n + 96) return count;
+    if (count <= 2 * n + 16) return count;
     const int tid = threadIdx.x;
     V mine[PER];
     uint32_t k[PER];
@@ -235,9 +261,34 @@ __device__ __forceinline__ int tighten(V* list, int count, int n, uint32_t* coun
     return (int)*left;
 }
 
+// The n best of the candidates found, best first; the entry's counter is free again.
+template <int PER>
+__device__ __forceinline__ void finish(const Args& a, Candidate* found, int there, int n, int entry, uint32_t* counts,
+                                       uint32_t* left, uint32_t* counter) {
+    const int tid = threadIdx.x;
+    const int count = tighten<PER>(found, there, n, counts, left, [](const Candidate& c) { return (uint32_t)(c.s >> 32); });
+    const int per = threads_per(count);
+    const int64_t out = (int64_t)entry * n;
+    for (int i = tid / per; i < count; i += kThreads / per) {
+        const Candidate c = found[i];
+        const int r = rank_of(found, count, c, per);
+        if (r < n && (tid & (per - 1)) == 0) {
+            a.tokens[out + r] = (int32_t)(0xFFFFFu - (uint32_t)(c.place & 0xFFFFFu));
+            a.parents[out + r] = 63 - (int32_t)(c.place >> 52);
+            a.scores_out[out + r] = (float)score_of(c.s);
+        }
+    }
+    if (tid >= count && tid < n) {
+        a.tokens[out + tid] = -1;
+        a.parents[out + tid] = -1;
+        a.scores_out[out + tid] = -INFINITY;
+    }
+    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // RUNS runs of eight values a thread, at most N choices.
 template <int TYPE, int RUNS, int N>
-__global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
+__global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
     extern __shared__ uint64_t lds[];
     __shared__ float part_m[kThreads / 64], part_s[kThreads / 64], part_t[kThreads / 64];
     __shared__ double offset[SGEMV_MAX_BEAMS];
@@ -256,31 +307,54 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
     if (!done) {
         const uint8_t* row = a.logits + (entry * a.ld_batch + beam * a.ld_beam) * ES;
         const int first = part * a.slice, end = first + a.slice < a.vocab ? first + a.slice : a.vocab;
-        float v[RUNS][8], run_top[RUNS];
+        float v[RUNS][8];
+        int base[RUNS];   // place of a run's first value
+        if (a.vocab >= 8) {
+            // a run that passes the end is read from eight before it, and what belongs to others is left out: loads
+            // without a branch are all in flight at once
+            Run<TYPE> raw[RUNS];
 #pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            const int at = first + (r * kThreads + tid) * 8;
-            if (at + 8 <= end) {
-                load8<TYPE>(row + (int64_t)at * ES, v[r]);
-            } else {
+            for (int r = 0; r < RUNS; ++r) {
+                const int at = first + (r * kThreads + tid) * 8;
+                base[r] = at < end - 8 ? at : end - 8;
+                raw[r].load(row + (int64_t)base[r] * ES);
+            }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[r][j] = at + j >= end ? -INFINITY
-                              : TYPE == SGEMV_F32
-                                  ? widen<TYPE>(reinterpret_cast<const uint32_t*>(row)[at + j])
-                                  : widen<TYPE>(reinterpret_cast<const uint16_t*>(row)[at + j]);
+            for (int r = 0; r < RUNS; ++r) {
+                const int at = first + (r * kThreads + tid) * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[r][j] = raw[r].get(j);
+                if (base[r] < at) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (base[r] + j < at) v[r][j] = -INFINITY;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < RUNS; ++r) {
+                base[r] = (r * kThreads + tid) * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[r][j] = -INFINITY;
+                    if (base[r] + j < end)
+                        v[r][j] = TYPE == SGEMV_F32 ? widen<TYPE>(reinterpret_cast<const uint32_t*>(row)[base[r] + j])
+                                                    : widen<TYPE>(reinterpret_cast<const uint16_t*>(row)[base[r] + j]);
+                }
             }
         }
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RUNS; ++r) {
-            run_top[r] = v[r][0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) run_top[r] = fmaxf(run_top[r], v[r][j]);
-            top = fmaxf(top, run_top[r]);
+            top = max3(top, v[r][0], v[r][1]);
+            top = max3(top, v[r][2], v[r][3]);
+            top = max3(top, v[r][4], v[r][5]);
+            top = max3(top, v[r][6], v[r][7]);
         }
         const float wm = wave_max(top);
-        const uint32_t nth = nth_of_wave<32 - kFixed<TYPE>>(key_of<TYPE>(top), n);
+        // wavefronts whose 64 lanes all have values; where there is none, the first one's may do alone
+        const int full = end - first >= 4 * 512 ? 4 : end - first >= 512 ? (end - first) / 512 : 1;
+        const uint32_t nth = nth_of_wave<32 - kFixed<TYPE>>(key_of<TYPE>(top), (n + full - 1) / full);
         if (lane == 0) {
             part_m[wave] = wm;
             part_t[wave] = nth ? value_of<TYPE>(nth) : -3.4028234664e38f;   // no bound: any finite value
@@ -294,39 +368,75 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
 #pragma unroll
         for (int w = 1; w < kThreads / 64; ++w) {
             m = fmaxf(m, part_m[w]);
-            least = fmaxf(least, part_t[w]);
+            least = w < full ? fminf(least, part_t[w]) : least;
         }
-        const float from = m == -INFINITY ? 0.0f : m;
-        float sum = 0.0f;
+        // 2^(v L - c), c the largest v L as a float: one rounding each, and none of the largest logit's own
+        float c = m == -INFINITY ? 0.0f : m * kLog2e, sum = 0.0f;
 #pragma unroll
         for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += __builtin_amdgcn_exp2f((v[r][j] - from) * 1.44269504e+0f);
+            for (int j = 0; j < 8; ++j) sum += __builtin_amdgcn_exp2f(fmaf(v[r][j], kLog2e, -c));
         sum = wave_sum(sum);
-        if (sum != sum) {   // NaN among the logits is left out; an infinity stays
+        if (lane == 0) part_s[wave] = sum;
+        __syncthreads();
+        sum = part_s[0];
+#pragma unroll
+        for (int w = 1; w < kThreads / 64; ++w) sum += part_s[w];
+        if (sum != sum) {   // the same in every thread: NaN among the logits is left out, an infinity stays
+            m = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = v[r][j] > m ? v[r][j] : m;
+            m = wave_max(m);
+            __syncthreads();
+            if (lane == 0) part_m[wave] = m;
+            __syncthreads();
+            m = part_m[0];
+#pragma unroll
+            for (int w = 1; w < kThreads / 64; ++w) m = fmaxf(m, part_m[w]);
+            c = m == -INFINITY ? 0.0f : m * kLog2e;
             sum = 0.0f;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (v[r][j] == v[r][j]) sum += __builtin_amdgcn_exp2f((v[r][j] - from) * 1.44269504e+0f);
+                    if (v[r][j] == v[r][j]) sum += __builtin_amdgcn_exp2f(fmaf(v[r][j], kLog2e, -c));
             sum = wave_sum(sum);
+            if (lane == 0) part_s[wave] = sum;
+            __syncthreads();
+            sum = part_s[0];
+#pragma unroll
+            for (int w = 1; w < kThreads / 64; ++w) sum += part_s[w];
         }
-        if (lane == 0) part_s[wave] = sum;
-        const auto place = [&](int r, int j) { return ~(uint32_t)(first + (r * kThreads + tid) * 8 + j); };
-        const uint32_t room = kMostTied;
+        const auto place = [&](int r, int j) { return ~(uint32_t)(base[r] + j); };
+        // values that reach the bound, each wavefront's in a place of its own
+        constexpr uint32_t kRoom = kMostTied / (kThreads / 64);
+        uint32_t many = 0;
 #pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-            if (!(run_top[r] >= least)) continue;
+        for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (v[r][j] >= least) {
-                    const uint32_t at = atomicAdd(&left, 1u);
-                    if (at < room) lds[at] = (uint64_t)key_of<TYPE>(v[r][j]) << 32 | place(r, j);
+            for (int j = 0; j < 8; ++j) {
+                const uint64_t reach = __ballot(v[r][j] >= least);
+                if (reach) {
+                    if (v[r][j] >= least) {
+                        const uint32_t to = many + __builtin_amdgcn_mbcnt_hi((uint32_t)(reach >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)reach, 0));
+                        if (to < kRoom) lds[wave * kRoom + to] = (uint64_t)key_of<TYPE>(v[r][j]) << 32 | place(r, j);
+                    }
+                    many += (uint32_t)__popcll(reach);
                 }
-        }
+            }
+        if (lane == 0) wave_bound[wave] = many;
         __syncthreads();
-        if (left > room) {   // the same in every thread
+        uint32_t of_wave[kThreads / 64], all = 0;
+        bool over = false;
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) {
+            of_wave[w] = wave_bound[w];
+            over = over || of_wave[w] > kRoom;
+            all += of_wave[w];
+        }
+        if (over) {   // the same in every thread
             __syncthreads();
             uint64_t best = 0;
 #pragma unroll
@@ -353,9 +463,30 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
                     }
             }
             __syncthreads();
+            all = left;
+        } else {      // side by side
+            constexpr int kEach = kMostTied / kThreads;
+            uint64_t mine_of[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t x = tid + i * kThreads, w = 0;
+                if (x >= all) break;
+#pragma unroll
+                for (int k = 0; k < kThreads / 64 - 1; ++k)
+                    if (w == (uint32_t)k && x >= of_wave[k]) {
+                        x -= of_wave[k];
+                        ++w;
+                    }
+                mine_of[i] = lds[w * kRoom + x];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (tid + i * kThreads < (int)all) lds[tid + i * kThreads] = mine_of[i];
+            __syncthreads();
         }
         constexpr int kMost = N * RUNS * 8 > kMostTied ? N * RUNS * 8 : kMostTied;
-        const int count = tighten<kMost / kThreads>(lds, (int)left, n, counts, &left, [](uint64_t k) { return (uint32_t)(k >> 32); });
+        const int count = tighten<kMost / kThreads>(lds, (int)all, n, counts, &left, [](uint64_t k) { return (uint32_t)(k >> 32); });
         const int per = threads_per(count);
         for (int i = tid / per; i < count; i += kThreads / per) {
             const uint64_t key = lds[i];
@@ -363,12 +494,7 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
             if (rank < n && (tid & (per - 1)) == 0) publish(mine + rank, key);
         }
         if (tid >= count && tid < n) publish(mine + tid, 0ull);
-        if (tid == 0) {
-            float s = part_s[0];
-#pragma unroll
-            for (int w = 1; w < kThreads / 64; ++w) s += part_s[w];
-            publish(mine + n, (uint64_t)__builtin_bit_cast(uint32_t, m) << 32 | __builtin_bit_cast(uint32_t, s));
-        }
+        if (tid == 0) publish(mine + n, (uint64_t)as_u32(m == -INFINITY ? m : c) << 32 | as_u32(sum));
     }
 
     // the last workgroup of this entry goes on
@@ -402,10 +528,11 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
                 for (int p = tid & 15; p < a.parts; p += 16) {
                     const uint64_t ms = lds[w * a.parts + p];
                     const float pm = __builtin_bit_cast(float, (uint32_t)(ms >> 32)), ps = __builtin_bit_cast(float, (uint32_t)ms);
-                    if (pm > -INFINITY) s += (double)(ps * __builtin_amdgcn_exp2f((pm - m) * 1.44269504e+0f));
+                    if (pm > -INFINITY) s += (double)(ps * __builtin_amdgcn_exp2f(pm - m));
                 }
                 s = row_sum(s);
-                off -= (double)m + log(s);   // not finite where no logit or an infinite one is there
+                // back by the factor that the exponents were taken with; not finite where no logit or an infinite one is there
+                off -= ((double)m + log2(s)) / (double)kLog2e;
             }
             if ((tid & 15) == 0) offset[w] = off;
         }
@@ -455,7 +582,7 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
     const int holders = (int)left, per_holder = threads_per(holders);
     for (int i = tid / per_holder; i < holders; i += kThreads / per_holder) {
         const Candidate c = found[i];
-        const int r = rank_of(found, holders, c, per_holder, above);
+        const int r = rank_of(found, holders, c, per_holder);
         if (r < n) order[r] = found_list[i];
         if (r == n - 1) bound = c;
     }
@@ -480,25 +607,7 @@ __global__ __launch_bounds__(kThreads, N == 16 ? 6 : 4) void k_beam(Args a) {
         if (c.s && !above(least, c)) found[atomicAdd(&left, 1u)] = c;
     }
     __syncthreads();
-    constexpr int kMostFound = (N * (N + 1) / 2 + kThreads - 1) / kThreads;
-    const int count = tighten<kMostFound>(found, (int)left, n, counts, &left, [](const Candidate& c) { return (uint32_t)(c.s >> 32); });
-    const int per = threads_per(count);
-    const int64_t out = (int64_t)entry * n;
-    for (int i = tid / per; i < count; i += kThreads / per) {
-        const Candidate c = found[i];
-        const int r = rank_of(found, count, c, per, above);
-        if (r < n && (tid & (per - 1)) == 0) {
-            a.tokens[out + r] = (int32_t)(0xFFFFFu - (uint32_t)(c.place & 0xFFFFFu));
-            a.parents[out + r] = 63 - (int32_t)(c.place >> 52);
-            a.scores_out[out + r] = (float)score_of(c.s);
-        }
-    }
-    if (tid >= count && tid < n) {
-        a.tokens[out + tid] = -1;
-        a.parents[out + tid] = -1;
-        a.scores_out[out + tid] = -INFINITY;
-    }
-    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    finish<(N * (N + 1) / 2 + kThreads - 1) / kThreads>(a, found, (int)left, n, entry, counts, &left, counter);
 }
 
 int64_t parts_of(int vocab, int runs) { return (vocab + runs * kThreads * 8 - 1) / (runs * kThreads * 8); }
