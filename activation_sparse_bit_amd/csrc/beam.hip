@@ -184,7 +184,7 @@ struct Candidate {
     uint64_t s, place;
 };
 __device__ __forceinline__ bool above(const Candidate& a, const Candidate& b) {
-    return a.s > b.s || (a.s == b.s && a.place > b.place);
+    return (a.s > b.s) | ((a.s == b.s) & (a.place > b.place));   // without branches
 }
 
 // Rank of item i of a list of `count` in LDS, counted by `per` neighbouring
@@ -197,25 +197,6 @@ __device__ __forceinline__ int rank_of(const V* list, int count, const V& item, 
     for (int d = 1; d < per; d <<= 1) rank += __shfl_xor(rank, d);
     return rank;
 }
-// The same for candidates: by the upper half of s, and by all of it where another has the same.
-__device__ __forceinline__ int rank_of(const Candidate* list, int count, const Candidate& item, int per) {
-    const uint32_t mine = (uint32_t)(item.s >> 32);
-    const uint32_t* upper = reinterpret_cast<const uint32_t*>(list) + 1;
-    int rank = 0, same = 0;
-#pragma unroll 8
-    for (int k = (int)threadIdx.x & (per - 1); k < count; k += per) {
-        const uint32_t other = upper[4 * k];
-        rank += other > mine;
-        same += other == mine;
-    }
-    for (int d = 1; d < per; d <<= 1) {
-        rank += __shfl_xor(rank, d);
-        same += __shfl_xor(same, d);
-    }
-    if (same > 1)   // the same in all threads of an item
-        rank = rank_of(list, count, item, per, above);
-    return rank;
-}
 // Threads that count together for each of `count` items.
 __device__ __forceinline__ int threads_per(int count) {
     int per = 1;
@@ -224,54 +205,59 @@ __device__ __forceinline__ int threads_per(int count) {
 }
 
 // Drops items that cannot be among the n best of a list of up to PER * kThreads
-// in LDS: those below the n-th largest key, found bit by bit.  Ranking is
-// quadratic, so it pays from some dozen items on.  Returns the new count.
+// in LDS: every wavefront finds the n/4-th largest key of its share, bit by bit,
+// and n items reach the smallest of these.  Ranking is quadratic, so it pays from
+// some dozen items on.  Returns the new count.
 template <int PER, class V, class F>
-__device__ __forceinline__ int tighten(V* list, int count, int n, uint32_t* counts, uint32_t* left, F key) {
-    if (count <= 2 * n + 16) return count;
+__device__ __forceinline__ int tighten(V* list, int count, int most, int n, uint32_t* bounds, uint32_t* left, F key) {
+    if (count <= most) return count;   // most is at least n, so every wavefront's share has n/4 items
     const int tid = threadIdx.x;
+    constexpr int kWaves = kThreads / 64;
+    const int at = (tid & 63) * kWaves + tid / 64;   // neighbours, which are alike, over the wavefronts
     V mine[PER];
     uint32_t k[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         k[i] = 0;
-        if (tid + i * kThreads < count) {
-            mine[i] = list[tid + i * kThreads];
+        if (at + i * kThreads < count) {
+            mine[i] = list[at + i * kThreads];
             k[i] = key(mine[i]);
         }
     }
-    if (tid < 32) counts[tid] = 0;
-    if (tid == 32) *left = 0;
-    __syncthreads();
     uint32_t t = 0;
+    const int need = (n + kWaves - 1) / kWaves;
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t trial = t | 1u << bit;
         int here = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (i * kThreads < count) here += lanes(k[i] >= trial);
-        if ((tid & 63) == 0 && here) atomicAdd(&counts[bit], (uint32_t)here);
-        __syncthreads();
-        if (counts[bit] >= (uint32_t)n) t = trial;
+        if (here >= need) t = trial;
     }
+    if ((tid & 63) == 0) bounds[tid / 64] = t;
+    if (tid == 0) *left = 0;
+    __syncthreads();
+    t = bounds[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) t = t < bounds[w] ? t : bounds[w];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        if (tid + i * kThreads < count && k[i] >= t) list[atomicAdd(left, 1u)] = mine[i];
+        if (at + i * kThreads < count && k[i] >= t) list[atomicAdd(left, 1u)] = mine[i];
     __syncthreads();
     return (int)*left;
 }
 
 // The n best of the candidates found, best first; the entry's counter is free again.
 template <int PER>
-__device__ __forceinline__ void finish(const Args& a, Candidate* found, int there, int n, int entry, uint32_t* counts,
+__device__ __forceinline__ void finish(const Args& a, Candidate* found, int there, int n, int entry, uint32_t* bounds,
                                        uint32_t* left, uint32_t* counter) {
     const int tid = threadIdx.x;
-    const int count = tighten<PER>(found, there, n, counts, left, [](const Candidate& c) { return (uint32_t)(c.s >> 32); });
+    const int count = tighten<PER>(found, there, 2 * n + 96, n, bounds, left, [](const Candidate& c) { return (uint32_t)(c.s >> 32); });
     const int per = threads_per(count);
     const int64_t out = (int64_t)entry * n;
     for (int i = tid / per; i < count; i += kThreads / per) {
         const Candidate c = found[i];
-        const int r = rank_of(found, count, c, per);
+        const int r = rank_of(found, count, c, per, above);
         if (r < n && (tid & (per - 1)) == 0) {
             a.tokens[out + r] = (int32_t)(0xFFFFFu - (uint32_t)(c.place & 0xFFFFFu));
             a.parents[out + r] = 63 - (int32_t)(c.place >> 52);
@@ -292,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
     extern __shared__ uint64_t lds[];
     __shared__ float part_m[kThreads / 64], part_s[kThreads / 64], part_t[kThreads / 64];
     __shared__ double offset[SGEMV_MAX_BEAMS];
-    __shared__ uint32_t left, counts[32], wave_bound[kThreads / 64], order[N];
+    __shared__ uint32_t left, bounds[kThreads / 64], wave_bound[kThreads / 64], order[N];
     __shared__ uint64_t part_bound;
     __shared__ Candidate bound;
     constexpr int ES = TYPE == SGEMV_F32 ? 4 : 2;
@@ -486,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
             __syncthreads();
         }
         constexpr int kMost = N * RUNS * 8 > kMostTied ? N * RUNS * 8 : kMostTied;
-        const int count = tighten<kMost / kThreads>(lds, (int)all, n, counts, &left, [](uint64_t k) { return (uint32_t)(k >> 32); });
+        const int count = tighten<kMost / kThreads>(lds, (int)all, 256, n, bounds, &left, [](uint64_t k) { return (uint32_t)(k >> 32); });
         const int per = threads_per(count);
         for (int i = tid / per; i < count; i += kThreads / per) {
             const uint64_t key = lds[i];
@@ -582,7 +568,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
     const int holders = (int)left, per_holder = threads_per(holders);
     for (int i = tid / per_holder; i < holders; i += kThreads / per_holder) {
         const Candidate c = found[i];
-        const int r = rank_of(found, holders, c, per_holder);
+        const int r = rank_of(found, holders, c, per_holder, above);
         if (r < n) order[r] = found_list[i];
         if (r == n - 1) bound = c;
     }
@@ -607,7 +593,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
         if (c.s && !above(least, c)) found[atomicAdd(&left, 1u)] = c;
     }
     __syncthreads();
-    finish<(N * (N + 1) / 2 + kThreads - 1) / kThreads>(a, found, (int)left, n, entry, counts, &left, counter);
+    finish<(N * (N + 1) / 2 + kThreads - 1) / kThreads>(a, found, (int)left, n, entry, bounds, &left, counter);
 }
 
 int64_t parts_of(int vocab, int runs) { return (vocab + runs * kThreads * 8 - 1) / (runs * kThreads * 8); }
