@@ -14,12 +14,14 @@
 // a lane that reads eight tokens' eight elements turns them by byte permutes
 // into eight operands of eight tokens each.
 //
-// Work is split evenly whatever the lengths: all sequences' units of 128
-// tokens, sequence by sequence and head by head, form one line that is cut
-// into equal runs, one for each workgroup.  A run's first and last piece may
-// be part of a head; such pieces go to the workspace, and the last workgroup
-// of that head to arrive joins them in the order of the tokens.  The cut
-// follows from the lengths alone, so results do not depend on timing.
+// Work is split evenly whatever the lengths: the units of 128 tokens of all
+// sequences form one line that is cut into equal runs, and a workgroup takes
+// one run for one key head.  Neighbouring workgroups take the same run for
+// neighbouring heads, so rows of memory that hold several heads are read at
+// one time.  A run's first and last piece may be part of a sequence; such
+// pieces go to the workspace, and the last workgroup of that sequence and head
+// to arrive joins them in the order of the tokens.  The cut follows from the
+// lengths alone, so results do not depend on timing.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -43,10 +45,10 @@ constexpr int kWaves = 4;
 constexpr int kTile = 32;                 // tokens of a wavefront's step
 constexpr int kUnit = kWaves * kTile;     // tokens of a workgroup's step
 constexpr int kRows = 16;                 // query heads of one key head at a time
-constexpr int kMaxPieces = 128;           // of one head
+constexpr int kMaxRuns = 256;             // that the line is cut into, and so pieces of one head
 constexpr int kMaxHeads = 4096;           // heads (of all sequences) of one launch
 constexpr int kCounterStep = 16;          // words between arrival counters
-constexpr int kGrid = 1024;
+constexpr int kGrid = 512;                // workgroups that the GPU holds at once, two on a compute unit
 constexpr size_t kCounterBytes = (size_t)kMaxHeads * kCounterStep * 4;
 constexpr uint32_t kCacheSC1 = 16;        // cache policy: coherent at device scope
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -68,7 +70,7 @@ struct Args {
     int64_t q_row, q_head, out_row, out_head, ld_table;
     SgemvDiv page;
     int32_t pages, capacity;      // pages of the cache, tokens that a table's row can list
-    int32_t batch, heads, groups, group, tiles;   // query heads, key heads x tiles, heads a key head, tiles of 16
+    int32_t batch, heads, groups, group, kv_heads;   // query heads, key heads x tiles of 16, query heads a key head
     int32_t dim, window;
     int32_t q_vector;             // whether q can be read in 16 bytes
     uint32_t partial_bytes, slot_bytes;
@@ -162,16 +164,26 @@ struct Attention {
     struct Shared {
         union {
             float o[kWaves][kRows][LDO];
-            float2 join[kRows][kMaxPieces];               // weight (first the maximum) and sum of every piece
+            float2 join[kRows][kMaxRuns];               // weight (first the maximum) and sum of every piece
         };
         float m[kWaves][kRows], l[kWaves][kRows];
         float row_m[kRows], row_l[kRows];
-        int scan[kWaves], most[kWaves], found[2];
+        float4_t shares[256];
+        int scan[kWaves], found[2];
         int last;
     };
 
-    uint4_t kr[2][KLOADS];
-    uint32_t vr[8][VB][VWORDS];
+    // A step's keys and values as they come.
+    struct Tile {
+        uint4_t kr[2][KLOADS];
+        uint32_t vr[8][VB][VWORDS];
+    };
+    // Where a step's tokens are: the pages of its halves and the places there, or each lane's own page and place.
+    struct Where {
+        int id[2], in[2];
+        bool bad;
+    };
+
     typename T::frag qf[STEPS];
     float4_t o[VB][VW];
     float m, l;
@@ -203,13 +215,13 @@ struct Attention {
         }
     }
 
-    __device__ __forceinline__ void load_key(const Args& a, int which, const uint8_t* row, int g) {
+    static __device__ __forceinline__ void load_key(const Args& a, uint4_t (&kr)[KLOADS], const uint8_t* row, int g) {
 #pragma unroll
         for (int s = 0; s < KLOADS; ++s) {
             const int d = E4M3 ? 64 * s + 16 * g : 32 * s + 8 * g, n = E4M3 ? 16 : 8;
             const bool inside = E4M3 ? s < PAIRS - 1 : s < STEPS - 2;   // of any head that this kernel serves
             if (inside || a.dim == PAIRS * 64 || d + n <= a.dim) {
-                kr[which][s] = load16(row + d * ES);
+                kr[s] = load16(row + d * ES);
             } else {   // beyond a head's end: zero, since what stands there may be anything
                 uint4_t w = {0, 0, 0, 0};
                 if (E4M3 && d + 8 <= a.dim) {
@@ -217,12 +229,12 @@ struct Attention {
                     w[0] = half[0];
                     w[1] = half[1];
                 }
-                kr[which][s] = w;
+                kr[s] = w;
             }
         }
     }
 
-    __device__ __forceinline__ void load_value(const Args& a, int j, const uint8_t* row, int c) {
+    static __device__ __forceinline__ void load_value(const Args& a, uint32_t (&vr)[VB][VWORDS], const uint8_t* row, int c) {
 #pragma unroll
         for (int nb = 0; nb < VB; ++nb) {
             const int d = (nb * 16 + c) * VW;
@@ -230,61 +242,77 @@ struct Attention {
             if constexpr (VWORDS == 4) {
                 const uint4_t w = load16(p);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vr[j][nb][i] = w[i];
+                for (int i = 0; i < 4; ++i) vr[nb][i] = w[i];
             } else if constexpr (VWORDS == 2) {
                 const uint2_t w = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(p));
-                vr[j][nb][0] = w[0];
-                vr[j][nb][1] = w[1];
+                vr[nb][0] = w[0];
+                vr[nb][1] = w[1];
             } else {
-                vr[j][nb][0] = *reinterpret_cast<const uint32_t*>(p);
+                vr[nb][0] = *reinterpret_cast<const uint32_t*>(p);
             }
         }
     }
 
-    // One step: 32 tokens from t0 on, some of them in [lo, len).  Returns
-    // whether a page in use does not exist.
-    __device__ __forceinline__ bool step(const Args& a, const Span& span, const int32_t* pages, int64_t k_off,
-                                         int64_t v_off, int t0, float z_scale) {
-        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-        bool bad = false;
+    // The pages of 32 tokens from t0 on, some of them below len.
+    static __device__ __forceinline__ Where find(const Args& a, const int32_t* pages, int t0, int len) {
+        Where w;
+        w.bad = false;
         if constexpr (WHOLE) {
-            const int ta = t0, tb = t0 + 16 < span.len ? t0 + 16 : t0;
-            const int pa = divide(ta, a.page), pb = divide(tb, a.page);
-            int ia = pages[pa], ib = pages[pb];
-            if ((uint32_t)ia >= (uint32_t)a.pages) { bad = true; ia = 0; }
-            if ((uint32_t)ib >= (uint32_t)a.pages) { bad = true; ib = 0; }
-            const int oa = ta - pa * (int)a.page.d, ob = tb - pb * (int)a.page.d;
-            const uint8_t* ka = a.k + k_off + ia * a.k_page + oa * a.k_token;
-            const uint8_t* kb = a.k + k_off + ib * a.k_page + ob * a.k_token;
-            const uint8_t* va = a.v + v_off + ia * a.v_page + oa * a.v_token;
-            const uint8_t* vb = a.v + v_off + ib * a.v_page + ob * a.v_token;
-            load_key(a, 0, ka + c * a.k_token, g);
-            load_key(a, 1, kb + c * a.k_token, g);
+            const int t1 = t0 + 16 < len ? t0 + 16 : t0, p0 = divide(t0, a.page), p1 = divide(t1, a.page);
+            w.id[0] = pages[p0];
+            w.id[1] = pages[p1];
+            w.in[0] = t0 - p0 * (int)a.page.d;
+            w.in[1] = t1 - p1 * (int)a.page.d;
+        } else {
+            const int lane = threadIdx.x & 31, t = t0 + lane < len ? t0 + lane : len - 1, p = divide(t, a.page);
+            w.id[0] = pages[p];
+            w.in[0] = t - p * (int)a.page.d;
+        }
+        return w;
+    }
+
+    // Starts a step's loads.  An id that is no page becomes page 0, and `bad` says so.
+    static __device__ __forceinline__ void load(const Args& a, Tile& tile, Where w, int64_t k_off, int64_t v_off, bool& bad) {
+        const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+        if constexpr (WHOLE) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                load_value(a, j, va + (4 * g + j) * a.v_token, c);
-                load_value(a, 4 + j, vb + (4 * g + j) * a.v_token, c);
+            for (int h = 0; h < 2; ++h) {
+                if ((uint32_t)w.id[h] >= (uint32_t)a.pages) {
+                    bad = true;
+                    w.id[h] = 0;
+                }
+                const uint8_t* k = a.k + k_off + w.id[h] * a.k_page + w.in[h] * a.k_token;
+                load_key(a, tile.kr[h], k + c * a.k_token, g);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* v = a.v + v_off + w.id[h] * a.v_page + w.in[h] * a.v_token;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) load_value(a, tile.vr[4 * h + j], v + (4 * g + j) * a.v_token, c);
             }
         } else {
-            const int mine = t0 + (lane & 31) < span.len ? t0 + (lane & 31) : span.len - 1;
-            const int p = divide(mine, a.page);
-            int id = pages[p];
-            const int in = mine - p * (int)a.page.d;
-            if ((uint32_t)id >= (uint32_t)a.pages) { bad = true; id = 0; }
-            bad = __ballot(bad) != 0;
+            const bool out = (uint32_t)w.id[0] >= (uint32_t)a.pages;
+            bad |= __ballot(out) != 0;
+            if (out) w.id[0] = 0;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int i = __shfl(id, 16 * w + c), t = __shfl(in, 16 * w + c);
-                load_key(a, w, a.k + k_off + i * a.k_page + t * a.k_token, g);
+            for (int h = 0; h < 2; ++h) {
+                const int i = __shfl(w.id[0], 16 * h + c), t = __shfl(w.in[0], 16 * h + c);
+                load_key(a, tile.kr[h], a.k + k_off + i * a.k_page + t * a.k_token, g);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int from = 16 * (j >> 2) + 4 * g + (j & 3);
-                const int i = __shfl(id, from), t = __shfl(in, from);
-                load_value(a, j, a.v + v_off + i * a.v_page + t * a.v_token, c);
+                const int i = __shfl(w.id[0], from), t = __shfl(w.in[0], from);
+                load_value(a, tile.vr[j], a.v + v_off + i * a.v_page + t * a.v_token, c);
             }
         }
+    }
 
+    // One step with keys and values that were loaded: 32 tokens from t0 on, some of them in [lo, len).
+    __device__ __forceinline__ void step(const Args& a, Tile& tile, const Span& span, int t0, float z_scale) {
+        const int lane = threadIdx.x & 63, g = lane >> 4;
+        uint4_t (&kr)[2][KLOADS] = tile.kr;
+        uint32_t (&vr)[8][VB][VWORDS] = tile.vr;
         float4_t z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -381,23 +409,41 @@ struct Attention {
         for (int nb = 0; nb < VB; ++nb)
 #pragma unroll
             for (int r = 0; r < VW; ++r) asm volatile("" : "+v"(o[nb][r]));
-        return bad;
     }
 
-    // Joins the pieces of a head, in the order of their tokens.
-    static __device__ void join(const Args& a, Shared& sh, __amdgpu_buffer_rsrc_t rs, int w0, int pieces, int run,
-                                int start, int rows) {
-        const int tid = threadIdx.x, row = tid >> 4, sub = tid & 15;
-        const auto slot = [&](int i) {   // a run that starts before this head ends with it: its second slot
+    // Joins the pieces of a head, in the order of their tokens: weights of the pieces' sums in LDS, then outputs.  The
+    // first pieces' outputs are under way while the weights are made.
+    static __device__ void join(const Args& a, Shared& sh, __amdgpu_buffer_rsrc_t rs, int w0, int pieces, int run, int start,
+                                int h, int rows, int b, int head0, float v_by) {
+        constexpr int kAtOnce = 16;
+        const int tid = threadIdx.x;
+        const auto slot = [&](int i) {   // a run that starts before this sequence ends with it: its second slot
             const int w = w0 + i;
-            return (uint32_t)(2 * w + (w * run < start ? 1 : 0)) * a.slot_bytes;
+            return (uint32_t)(2 * (w * a.groups + h) + (w * run < start ? 1 : 0)) * a.slot_bytes;
         };
+        const int quads = a.dim / 4, items = rows * quads;
+        int split = 1;   // threads that share an item's pieces
+        while (split < 8 && items * split * 2 <= 256) split *= 2;
+        const int part = tid / items;   // of the first items, when they are split
+        const auto fetch = [&](int row, int d, int from, int step, uint4_t (&w)[kAtOnce]) {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = from + k * step;
+                if (i < pieces) w[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, slot(i) + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
+            }
+        };
+        uint4_t early[kAtOnce];
+        const int first = split > 1 ? tid % items : tid;
+        const bool takes = split > 1 ? part < split : tid < items;
+        const int first_row = first / quads, first_d = 4 * (first - first_row * quads);
+        if (takes) fetch(first_row, first_d, split > 1 ? part : 0, split, early);
+
+        const int row = tid >> 4, sub = tid & 15;
         float top = -INFINITY;
         if (row < rows) {
             for (int i = sub; i < pieces; i += 16) {
-                const uint32_t at = slot(i) + kRows * DPAD * 4 + row * 8;
-                const float pm = as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, kCacheSC1));
-                const float pl = as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at + 4, 0, kCacheSC1));
+                const auto ml = __builtin_amdgcn_raw_buffer_load_b64(rs, slot(i) + kRows * DPAD * 4 + row * 8, 0, kCacheSC1);
+                const float pm = as_float(ml[0]), pl = as_float(ml[1]);
                 sh.join[row][i] = make_float2(pm, pl);
                 top = fmaxf(top, pm);
             }
@@ -419,6 +465,41 @@ struct Attention {
             }
         }
         __syncthreads();
+        const auto add = [&](float4_t& sum, int row, int from, int step, const uint4_t (&w)[kAtOnce]) {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = from + k * step;
+                if (i < pieces) sum += __builtin_bit_cast(float4_t, w[k]) * sh.join[row][i].x;
+            }
+        };
+        for (int x = first; takes && x < items; x += 256) {
+            const int r = x == first ? first_row : x / quads, d = x == first ? first_d : 4 * (x - r * quads);
+            float4_t sum = {0, 0, 0, 0};
+            for (int from = split > 1 ? part : 0; from < pieces; from += kAtOnce * split) {
+                uint4_t w[kAtOnce];
+                if (x == first && from < split) {
+                    add(sum, r, from, split, early);
+                } else {
+                    fetch(r, d, from, split, w);
+                    add(sum, r, from, split, w);
+                }
+            }
+            if (split == 1) {
+                store4(a, b, head0 + r, d, sum, v_by / sh.row_l[r]);
+            } else {
+                sh.shares[tid] = sum;
+            }
+        }
+        if (split > 1) {
+            __syncthreads();
+            if (tid < items) {
+                float4_t sum = sh.shares[tid];
+                for (int k = 1; k < split; ++k) sum += sh.shares[k * items + tid];
+                store4(a, b, head0 + first_row, first_d, sum, v_by / sh.row_l[first_row]);
+            }
+        }
+        if (a.lse && tid < rows)
+            a.lse[(int64_t)b * a.heads + head0 + tid] = kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
     }
 
     static __device__ __forceinline__ void store4(const Args& a, int b, int head, int d, float4_t v, float by) {
@@ -430,64 +511,71 @@ struct Attention {
     __device__ void run(const Args& a, Shared& sh) {
         const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
 
-        // the cut: units before every sequence, and the sequence of this run's first unit
-        const int each = (a.batch + 255) / 256;
-        int mine = 0, most = 0;
-        for (int i = 0; i < each; ++i) {
-            const int b = tid * each + i;
-            const int n = b < a.batch ? span_of(a.lengths[b], a).units : 0;
-            mine += n;
-            most = most > n ? most : n;
-        }
-        int scan = mine;
+        // the cut: this workgroup's head, the units before every sequence, and the sequence of its run's first unit
+        const int runs = (int)gridDim.x / a.groups, which = (int)blockIdx.x / a.groups, h = (int)blockIdx.x - which * a.groups;
+        int b, base, total, run;
+        if (a.batch <= 64) {   // every wavefront for itself
+            const int mine = lane < a.batch ? span_of(a.lengths[lane], a).units : 0;
+            int scan = mine;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(scan, d), other = __shfl_xor(most, d);
-            if (lane >= d) scan += up;
-            most = most > other ? most : other;
-        }
-        if (lane == 63) {
-            sh.scan[wave] = scan;
-            sh.most[wave] = most;
-        }
-        __syncthreads();
-        int total = 0, before = scan - mine;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += sh.scan[w];
-            total += sh.scan[w];
-            most = most > sh.most[w] ? most : sh.most[w];
-        }
-        total = uniform(total) * a.groups;
-        const int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-        const int least = (uniform(most) + kMaxPieces - 2) / (kMaxPieces - 1);
-        const int run = share > least ? share : least;
-        int u = (int)blockIdx.x * run;
-        if (u >= total) return;
-        const int end = u + run < total ? u + run : total;
-        for (int i = 0; i < each; ++i) {
-            const int b = tid * each + i;
-            const int n = b < a.batch ? span_of(a.lengths[b], a).units : 0;
-            if (before * a.groups <= u && u < (before + n) * a.groups) {
-                sh.found[0] = b;
-                sh.found[1] = before * a.groups;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int up = __shfl_up(scan, d);
+                if (lane >= d) scan += up;
             }
-            before += n;
+            total = __builtin_amdgcn_readlane(scan, 63);
+            run = (total + runs - 1) / runs;
+            const uint64_t past = __ballot(scan > which * run);
+            if (!past) return;   // beyond the last unit
+            b = __builtin_ctzll(past);
+            base = __builtin_amdgcn_readlane(scan - mine, b);
+        } else {
+            const int each = (a.batch + 255) / 256;
+            int mine = 0;
+            for (int i = 0; i < each; ++i)
+                if (tid * each + i < a.batch) mine += span_of(a.lengths[tid * each + i], a).units;
+            int scan = mine;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int up = __shfl_up(scan, d);
+                if (lane >= d) scan += up;
+            }
+            if (lane == 63) sh.scan[wave] = scan;
+            __syncthreads();
+            int before = scan - mine;
+            total = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                if (w < wave) before += sh.scan[w];
+                total += sh.scan[w];
+            }
+            total = uniform(total);
+            run = (total + runs - 1) / runs;
+            const int at = which * run;
+            if (at >= total) return;
+            for (int i = 0; i < each; ++i) {
+                const int n = tid * each + i < a.batch ? span_of(a.lengths[tid * each + i], a).units : 0;
+                if (before <= at && at < before + n) {
+                    sh.found[0] = tid * each + i;
+                    sh.found[1] = before;
+                }
+                before += n;
+            }
+            __syncthreads();
+            b = uniform(sh.found[0]);
+            base = uniform(sh.found[1]);
         }
-        __syncthreads();
-        int b = uniform(sh.found[0]), base = uniform(sh.found[1]);
+        int u = which * run;
+        const int end = u + run < total ? u + run : total;
+        const int kvh = h % a.kv_heads, tile = h / a.kv_heads;
+        const int rows = a.group - kRows * tile < kRows ? a.group - kRows * tile : kRows;
+        const int head0 = kvh * a.group + kRows * tile;
         Span span = span_of(uniform(a.lengths[b]), a);
         const __amdgpu_buffer_rsrc_t rs =
             __builtin_amdgcn_make_buffer_rsrc(a.partial, (short)0, (int)a.partial_bytes, 0x00020000);
         int piece = 0;
 
         while (u < end) {
-            const int h = (u - base) / span.units, c0 = u - base - h * span.units;
-            const int start = u - c0;
-            const int c1 = span.units < c0 + (end - u) ? span.units : c0 + (end - u);
-            const int kvh = h / a.tiles, tile = h - kvh * a.tiles;
-            const int rows = a.group - kRows * tile < kRows ? a.group - kRows * tile : kRows;
-            const int head0 = kvh * a.group + kRows * tile;
+            const int c0 = u - base, c1 = span.units < c0 + (end - u) ? span.units : c0 + (end - u);
             load_q(a, b, head0 + (c < rows ? c : 0), g);
             float z_scale = a.scale * kLog2e;
             if (a.softcap > 0.0f) z_scale = a.scale;
@@ -500,9 +588,14 @@ struct Attention {
                 for (int r = 0; r < VW; ++r) o[nb][r] = float4_t{0, 0, 0, 0};
             bool bad = span.bad;
             const int32_t* pages = a.table + b * a.ld_table;
-            for (int i = c0; i < c1; ++i) {
-                const int t0 = span.first + i * kUnit + wave * kTile;
-                if (t0 < span.len) bad |= step(a, span, pages, kvh * a.k_head, kvh * a.v_head, t0, z_scale);
+            // this wavefront's steps of the piece: tokens t0, t0 + kUnit, ... below `last`
+            const int64_t k_off = kvh * a.k_head, v_off = kvh * a.v_head;
+            int t0 = span.first + c0 * kUnit + wave * kTile;
+            const int last = span.first + c1 * kUnit < span.len ? span.first + c1 * kUnit : span.len;
+            for (; t0 < last; t0 += kUnit) {
+                Tile tile;
+                load(a, tile, find(a, pages, t0, span.len), k_off, v_off, bad);
+                step(a, tile, span, t0, z_scale);
             }
             l = head_sum(l);
             if (bad) l = NAN;
@@ -570,41 +663,21 @@ struct Attention {
                 }
                 __builtin_amdgcn_s_waitcnt(0);   // this thread's stores acknowledged
                 __syncthreads();                 // ... and every thread's, before the count
-                const int w0 = start / run, pieces = (start + span.units - 1) / run - w0 + 1;
+                const int w0 = base / run, pieces = (base + span.units - 1) / run - w0 + 1;
                 uint32_t* counter = a.counters + (b * a.groups + h) * kCounterStep;
                 if (tid == 0)
                     sh.last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                               (uint32_t)(pieces - 1);
                 __syncthreads();
                 if (uniform(sh.last)) {
-                    join(a, sh, rs, w0, pieces, run, start, rows);
-                    const int quads = a.dim / 4;
-                    for (int x = tid; x < rows * quads; x += 256) {
-                        const int row = x / quads, d = 4 * (x - row * quads);
-                        float4_t sum = {0, 0, 0, 0};
-                        for (int i = 0; i < pieces; i += 8) {
-                            uint4_t w[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int at = i + k < pieces ? i + k : i, wg = w0 + at;
-                                const uint32_t s = (uint32_t)(2 * wg + (wg * run < start ? 1 : 0)) * a.slot_bytes;
-                                w[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, s + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (i + k < pieces) sum += __builtin_bit_cast(float4_t, w[k]) * sh.join[row][i + k].x;
-                        }
-                        store4(a, b, head0 + row, d, sum, v_by / sh.row_l[row]);
-                    }
-                    if (a.lse && tid < rows)
-                        a.lse[(int64_t)b * a.heads + head0 + tid] = kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
+                    join(a, sh, rs, w0, pieces, run, base, h, rows, b, head0, v_by);
                     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 }
                 __syncthreads();
             }
             u += c1 - c0;
             ++piece;
-            if (u < end && u == base + a.groups * span.units) {
+            if (u < end) {
                 base = u;
                 ++b;
                 span = span_of(uniform(a.lengths[b]), a);
@@ -614,7 +687,7 @@ struct Attention {
 };
 
 template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE>
-__global__ __launch_bounds__(256) void k_attn(Args a) {
+__global__ __launch_bounds__(256, PAIRS <= 2 ? 2 : 1) void k_attn(Args a) {
     using Op = Attention<T, E4M3, PAIRS, VW, VB, WHOLE>;
     __shared__ typename Op::Shared sh;
     Op op;
@@ -646,7 +719,8 @@ extern "C" size_t sgemv_attn_workspace_bytes(int32_t batch, int32_t heads, int32
     if (batch < 0 || heads < 1 || heads > SGEMV_MAX_HEADS || heads_kv < 1 || heads % heads_kv || dim < 8 ||
         dim > SGEMV_MAX_DIM || dim % 8)
         return 0;
-    return kCounterBytes + (size_t)2 * kGrid * slot_bytes(dim);
+    const int64_t groups = (int64_t)heads_kv * ((heads / heads_kv + kRows - 1) / kRows);
+    return kCounterBytes + (size_t)2 * (groups > kGrid ? groups : kGrid) * slot_bytes(dim);
 }
 
 extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cache, void* stream) {
@@ -709,19 +783,23 @@ extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cac
     a.capacity = p.max_pages * kv.page_size;
     a.heads = p.heads;
     a.group = p.heads / kv.heads;
-    a.tiles = (a.group + kRows - 1) / kRows;
-    a.groups = kv.heads * a.tiles;
+    a.kv_heads = kv.heads;
+    a.groups = kv.heads * ((a.group + kRows - 1) / kRows);
     a.dim = kv.dim;
     a.window = p.window;
     a.q_vector = sgemv_aligned(p.q, 16) && p.q_row % 8 == 0 && p.q_head % 8 == 0;
     a.slot_bytes = slot_bytes(kv.dim);
-    a.partial_bytes = 2 * kGrid * a.slot_bytes;
+    // a run for each workgroup that fits, for every head
+    int runs = kGrid / a.groups;
+    runs = runs < 1 ? 1 : runs > kMaxRuns ? kMaxRuns : runs;
+    const unsigned grid = (unsigned)(runs * a.groups);
+    a.partial_bytes = 2 * grid * a.slot_bytes;
     a.scale = p.scale;
     a.softcap = p.softcap;
     const bool whole_pages = kv.page_size % 16 == 0, e4m3 = kv.type == SGEMV_E4M3;
     const Kernel kernel = p.type == SGEMV_F16 ? pick<F16>(e4m3, whole_pages, kv.dim) : pick<BF16>(e4m3, whole_pages, kv.dim);
     // a launch counts its units in 30 bits and its heads by kMaxHeads counters
-    const int64_t units = (int64_t)a.groups * (a.capacity / kUnit + 2);
+    const int64_t units = a.capacity / kUnit + 2;
     int64_t per = kMaxHeads / a.groups;
     if (per > 0x3FFFFFFF / units) per = 0x3FFFFFFF / units;
     if (per < 1) return SGEMV_ESIZE;
@@ -733,7 +811,7 @@ extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cac
         a.table = p.table + b * p.ld_table;
         a.lengths = p.lengths + b;
         void* kargs[] = {&a};
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(kGrid), dim3(256), kargs, 0,
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(256), kargs, 0,
                                              static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return sgemv_hip_failed((int)e);
     }
