@@ -12,7 +12,13 @@
 // running maximum, its correction and the output belong to the lane's head.
 // Values are read in rows (16 bytes a lane, whole rows by neighbouring lanes);
 // a lane that reads eight tokens' eight elements turns them by byte permutes
-// into eight operands of eight tokens each.
+// into eight operands of eight tokens each.  Keys are read in whole lines of 128
+// bytes too, eight tokens a load, and two loads exchange half their lanes (eight
+// apart) to become the operands of 16 tokens.  Loads of whole lines can be
+// marked as used once (48 x 24000 tokens, 64 heads on 8: 752 us, 664 marked,
+// which is 6.5 TB/s); where a row is no whole number of lines, or several
+// workgroups read it, that costs more than it gives (heads of 96: 108 us
+// against 95; 20 heads a key head: 150 against 137).
 //
 // Work is split evenly whatever the lengths: the units of 128 tokens of all
 // sequences form one line that is cut into equal runs, and a workgroup takes
@@ -46,8 +52,9 @@ constexpr int kTile = 32;                 // tokens of a wavefront's step
 constexpr int kUnit = kWaves * kTile;     // tokens of a workgroup's step
 constexpr int kRows = 16;                 // query heads of one key head at a time
 constexpr int kMaxRuns = 256;             // that the line is cut into, and so pieces of one head
-constexpr int kMaxHeads = 4096;           // heads (of all sequences) of one launch
-constexpr int kCounterStep = 16;          // words between arrival counters
+constexpr int kParty = 16;                // pieces that are joined to one where there are more than twice as many
+constexpr int kMaxHeads = 2048;           // heads (of all sequences) of one launch
+constexpr int kCounterStep = 32;          // words between heads' arrival counters: one, and one for each party
 constexpr int kGrid = 512;                // workgroups that the GPU holds at once, two on a compute unit
 constexpr size_t kCounterBytes = (size_t)kMaxHeads * kCounterStep * 4;
 constexpr uint32_t kCacheSC1 = 16;        // cache policy: coherent at device scope
@@ -150,8 +157,9 @@ __device__ __forceinline__ Span span_of(int len, const Args& a) {
 
 // PAIRS: 64s of elements that a head's keys are padded to.  VW: value elements
 // of a lane, VB blocks of 16 of them.  WHOLE: page_size is a multiple of 16, so
-// 16 tokens from a multiple of 16 on lie in one page.
-template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE>
+// 16 tokens from a multiple of 16 on lie in one page.  LINES: heads of PAIRS * 64
+// elements, whole lines, each read once.
+template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE, bool LINES>
 struct Attention {
     static constexpr int STEPS = 2 * PAIRS;
     static constexpr int KLOADS = E4M3 ? PAIRS : STEPS;   // 16-byte loads of a token's row by four lanes
@@ -164,7 +172,10 @@ struct Attention {
     struct Shared {
         union {
             float o[kWaves][kRows][LDO];
-            float2 join[kRows][kMaxRuns];               // weight (first the maximum) and sum of every piece
+            struct {
+                float2 join[kRows][2 * kParty];           // weight (first the maximum) and sum of every part
+                float4_t sums[kRows][DPAD / 4];
+            };
         };
         float m[kWaves][kRows], l[kWaves][kRows];
         float row_m[kRows], row_l[kRows];
@@ -192,9 +203,28 @@ struct Attention {
         return __builtin_bit_cast(uint4_t, *reinterpret_cast<const uint4_u*>(p));
     }
 
+    static __device__ __forceinline__ uint4_t load16nt(const uint8_t* p) {
+        return __builtin_bit_cast(uint4_t, __builtin_nontemporal_load(reinterpret_cast<const uint4_u*>(p)));
+    }
     // First element of a lane's eight of step s.
     static __device__ __forceinline__ int key_dim(int s, int g) {
         return E4M3 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+    }
+    // Loads that pair up to whole lines; an odd one is loaded by token.
+    static constexpr int PAIRED = KLOADS / 2 * 2;
+
+    // 16 bytes of a key from element d on, zero beyond a head's end, since what stands there may be anything.
+    template <bool LAST, bool ONCE>
+    static __device__ __forceinline__ uint4_t key_piece(const Args& a, const uint8_t* row, int d) {
+        constexpr int n = E4M3 ? 16 : 8;
+        if (LINES || !LAST || a.dim == PAIRS * 64 || d + n <= a.dim) return ONCE && LINES ? load16nt(row + d * ES) : load16(row + d * ES);
+        uint4_t w = {0, 0, 0, 0};
+        if (E4M3 && d + 8 <= a.dim) {
+            const uint2_t half = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(row + d));
+            w[0] = half[0];
+            w[1] = half[1];
+        }
+        return w;
     }
 
     __device__ __forceinline__ void load_q(const Args& a, int b, int head, int g) {
@@ -215,36 +245,49 @@ struct Attention {
         }
     }
 
-    static __device__ __forceinline__ void load_key(const Args& a, uint4_t (&kr)[KLOADS], const uint8_t* row, int g) {
+    // The keys of 16 tokens: low is the lane's token of the first eight, high that of the second, own that of its number.
+    static __device__ __forceinline__ void load_key(const Args& a, uint4_t (&kr)[KLOADS], const uint8_t* low, const uint8_t* high,
+                                                    const uint8_t* own, int c, int g) {
+        constexpr int n = E4M3 ? 16 : 8;
 #pragma unroll
-        for (int s = 0; s < KLOADS; ++s) {
-            const int d = E4M3 ? 64 * s + 16 * g : 32 * s + 8 * g, n = E4M3 ? 16 : 8;
-            const bool inside = E4M3 ? s < PAIRS - 1 : s < STEPS - 2;   // of any head that this kernel serves
-            if (inside || a.dim == PAIRS * 64 || d + n <= a.dim) {
-                kr[s] = load16(row + d * ES);
-            } else {   // beyond a head's end: zero, since what stands there may be anything
-                uint4_t w = {0, 0, 0, 0};
-                if (E4M3 && d + 8 <= a.dim) {
-                    const uint2_t half = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(row + d));
-                    w[0] = half[0];
-                    w[1] = half[1];
-                }
-                kr[s] = w;
+        for (int s = 0; s < PAIRED; s += 2) {
+            const int d = 4 * n * (s + (c >> 3)) + n * g;
+            if (s + 2 < KLOADS) {
+                kr[s] = key_piece<false, true>(a, low, d);
+                kr[s + 1] = key_piece<false, true>(a, high, d);
+            } else {
+                kr[s] = key_piece<true, true>(a, low, d);
+                kr[s + 1] = key_piece<true, true>(a, high, d);
             }
         }
+        if constexpr (KLOADS > PAIRED) kr[PAIRED] = key_piece<true, false>(a, own, 4 * n * PAIRED + n * g);
+    }
+
+    // A pair of loads as the operands that they stand for: lanes 8..15 of each 16 of the one, 0..7 of the other change places.
+    static __device__ __forceinline__ void pair_up(uint4_t& even, uint4_t& odd) {
+        uint4_t x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = (int)even[i], o = (int)odd[i];
+            x[i] = (uint32_t)__builtin_amdgcn_update_dpp(e, o, 0x128 /* row_ror:8 */, 0xF, 0xC, false);
+            y[i] = (uint32_t)__builtin_amdgcn_update_dpp(o, e, 0x128, 0xF, 0x3, false);
+        }
+        even = x;
+        odd = y;
     }
 
     static __device__ __forceinline__ void load_value(const Args& a, uint32_t (&vr)[VB][VWORDS], const uint8_t* row, int c) {
 #pragma unroll
         for (int nb = 0; nb < VB; ++nb) {
             const int d = (nb * 16 + c) * VW;
-            const uint8_t* p = row + (d < a.dim ? d : 0) * ES;   // beyond a head's end: rows of the result that nobody reads
+            const uint8_t* p = row + (LINES || d < a.dim ? d : 0) * ES;   // beyond a head's end: rows of the result that nobody reads
             if constexpr (VWORDS == 4) {
-                const uint4_t w = load16(p);
+                const uint4_t w = LINES ? load16nt(p) : load16(p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) vr[nb][i] = w[i];
             } else if constexpr (VWORDS == 2) {
-                const uint2_t w = __builtin_bit_cast(uint2_t, *reinterpret_cast<const uint2_u*>(p));
+                const uint2_u* q = reinterpret_cast<const uint2_u*>(p);
+                const uint2_t w = __builtin_bit_cast(uint2_t, LINES ? __builtin_nontemporal_load(q) : *q);
                 vr[nb][0] = w[0];
                 vr[nb][1] = w[1];
             } else {
@@ -282,7 +325,7 @@ struct Attention {
                     w.id[h] = 0;
                 }
                 const uint8_t* k = a.k + k_off + w.id[h] * a.k_page + w.in[h] * a.k_token;
-                load_key(a, tile.kr[h], k + c * a.k_token, g);
+                load_key(a, tile.kr[h], k + (c & 7) * a.k_token, k + (8 + (c & 7)) * a.k_token, k + c * a.k_token, c, g);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -296,8 +339,14 @@ struct Attention {
             if (out) w.id[0] = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = __shfl(w.id[0], 16 * h + c), t = __shfl(w.in[0], 16 * h + c);
-                load_key(a, tile.kr[h], a.k + k_off + i * a.k_page + t * a.k_token, g);
+                const uint8_t* row[3];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    const int from = 16 * h + (x == 0 ? c & 7 : x == 1 ? 8 + (c & 7) : c);
+                    const int i = __shfl(w.id[0], from), t = __shfl(w.in[0], from);
+                    row[x] = a.k + k_off + i * a.k_page + t * a.k_token;
+                }
+                load_key(a, tile.kr[h], row[0], row[1], row[2], c, g);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -313,6 +362,10 @@ struct Attention {
         const int lane = threadIdx.x & 63, g = lane >> 4;
         uint4_t (&kr)[2][KLOADS] = tile.kr;
         uint32_t (&vr)[8][VB][VWORDS] = tile.vr;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int s = 0; s < PAIRED; s += 2) pair_up(kr[w][s], kr[w][s + 1]);
         float4_t z[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int w = 0; w < 2; ++w)
@@ -411,37 +464,40 @@ struct Attention {
             for (int r = 0; r < VW; ++r) asm volatile("" : "+v"(o[nb][r]));
     }
 
-    // Joins the pieces of a head, in the order of their tokens: weights of the pieces' sums in LDS, then outputs.  The
-    // first pieces' outputs are under way while the weights are made.
-    static __device__ void join(const Args& a, Shared& sh, __amdgpu_buffer_rsrc_t rs, int w0, int pieces, int run, int start,
-                                int h, int rows, int b, int head0, float v_by) {
-        constexpr int kAtOnce = 16;
+    static __device__ __forceinline__ void store4(const Args& a, int b, int head, int d, float4_t v, float by) {
+        uint16_t* p = a.out + b * a.out_row + head * a.out_head + d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = T::one(v[i] * by);
+    }
+
+    // Joins `count` parts of a head, in the order of their tokens: weights of the parts in LDS, then outputs, of which
+    // out(row, element, four of them) takes the sums.  The first parts' outputs are under way while the weights are made.
+    template <class Slot, class Out>
+    static __device__ __forceinline__ void join(const Args& a, Shared& sh, __amdgpu_buffer_rsrc_t rs, int count, int rows,
+                                                Slot slot, Out out) {
+        constexpr int kAtOnce = 8;
         const int tid = threadIdx.x;
-        const auto slot = [&](int i) {   // a run that starts before this sequence ends with it: its second slot
-            const int w = w0 + i;
-            return (uint32_t)(2 * (w * a.groups + h) + (w * run < start ? 1 : 0)) * a.slot_bytes;
-        };
         const int quads = a.dim / 4, items = rows * quads;
-        int split = 1;   // threads that share an item's pieces
+        int split = 1;   // threads that share an item's parts
         while (split < 8 && items * split * 2 <= 256) split *= 2;
-        const int part = tid / items;   // of the first items, when they are split
-        const auto fetch = [&](int row, int d, int from, int step, uint4_t (&w)[kAtOnce]) {
+        const int share = split > 1 ? tid / items : 0;
+        const auto fetch = [&](int row, int d, int from, uint4_t (&w)[kAtOnce]) {
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
-                const int i = from + k * step;
-                if (i < pieces) w[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, slot(i) + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
+                const int i = from + k * split;
+                if (i < count) w[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, slot(i) + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
             }
         };
-        uint4_t early[kAtOnce];
-        const int first = split > 1 ? tid % items : tid;
-        const bool takes = split > 1 ? part < split : tid < items;
+        uint4_t w[kAtOnce];
+        const int first = split > 1 ? tid - share * items : tid;
+        const bool takes = split > 1 ? share < split : tid < items;
         const int first_row = first / quads, first_d = 4 * (first - first_row * quads);
-        if (takes) fetch(first_row, first_d, split > 1 ? part : 0, split, early);
+        if (takes) fetch(first_row, first_d, share, w);
 
         const int row = tid >> 4, sub = tid & 15;
         float top = -INFINITY;
         if (row < rows) {
-            for (int i = sub; i < pieces; i += 16) {
+            for (int i = sub; i < count; i += 16) {
                 const auto ml = __builtin_amdgcn_raw_buffer_load_b64(rs, slot(i) + kRows * DPAD * 4 + row * 8, 0, kCacheSC1);
                 const float pm = as_float(ml[0]), pl = as_float(ml[1]);
                 sh.join[row][i] = make_float2(pm, pl);
@@ -451,11 +507,11 @@ struct Attention {
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
             const float base = top == -INFINITY ? 0.0f : top;
             float sum = 0.0f;
-            for (int i = sub; i < pieces; i += 16) {
+            for (int i = sub; i < count; i += 16) {
                 const float2 p = sh.join[row][i];
-                const float w = __builtin_amdgcn_exp2f(p.x - base);
-                sh.join[row][i].x = w;
-                sum += w * p.y;
+                const float by = __builtin_amdgcn_exp2f(p.x - base);
+                sh.join[row][i].x = by;
+                sum += by * p.y;
             }
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d);
@@ -465,47 +521,47 @@ struct Attention {
             }
         }
         __syncthreads();
-        const auto add = [&](float4_t& sum, int row, int from, int step, const uint4_t (&w)[kAtOnce]) {
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const int i = from + k * step;
-                if (i < pieces) sum += __builtin_bit_cast(float4_t, w[k]) * sh.join[row][i].x;
-            }
-        };
         for (int x = first; takes && x < items; x += 256) {
             const int r = x == first ? first_row : x / quads, d = x == first ? first_d : 4 * (x - r * quads);
             float4_t sum = {0, 0, 0, 0};
-            for (int from = split > 1 ? part : 0; from < pieces; from += kAtOnce * split) {
-                uint4_t w[kAtOnce];
-                if (x == first && from < split) {
-                    add(sum, r, from, split, early);
-                } else {
-                    fetch(r, d, from, split, w);
-                    add(sum, r, from, split, w);
-                }
+            for (int from = share; from < count; from += kAtOnce * split) {
+                if (x != first || from >= split) fetch(r, d, from, w);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    if (from + k * split < count) sum += __builtin_bit_cast(float4_t, w[k]) * sh.join[r][from + k * split].x;
             }
-            if (split == 1) {
-                store4(a, b, head0 + r, d, sum, v_by / sh.row_l[r]);
-            } else {
-                sh.shares[tid] = sum;
-            }
+            if (split == 1) out(r, d, sum);
+            else sh.shares[tid] = sum;
         }
         if (split > 1) {
             __syncthreads();
             if (tid < items) {
                 float4_t sum = sh.shares[tid];
                 for (int k = 1; k < split; ++k) sum += sh.shares[k * items + tid];
-                store4(a, b, head0 + first_row, first_d, sum, v_by / sh.row_l[first_row]);
+                out(first_row, first_d, sum);
             }
         }
-        if (a.lse && tid < rows)
-            a.lse[(int64_t)b * a.heads + head0 + tid] = kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
     }
 
-    static __device__ __forceinline__ void store4(const Args& a, int b, int head, int d, float4_t v, float by) {
-        uint16_t* p = a.out + b * a.out_row + head * a.out_head + d;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = T::one(v[i] * by);
+    // Counts the workgroup as one of n that have published; whether it is the last, which leaves the counter at zero.
+    static __device__ __forceinline__ bool arrive(Shared& sh, uint32_t* counter, int n) {
+        __builtin_amdgcn_s_waitcnt(0);   // this thread's stores acknowledged
+        __syncthreads();                 // ... and every thread's, before the count
+        if (threadIdx.x == 0) {
+            const bool last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(n - 1);
+            if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            sh.last = last;
+        }
+        __syncthreads();
+        return uniform(sh.last) != 0;
+    }
+
+    static __device__ __forceinline__ void publish_sums(Shared& sh, __amdgpu_buffer_rsrc_t rs, uint32_t slot, int rows) {
+        if ((int)threadIdx.x < rows) {
+            const uint32_t at = slot + kRows * DPAD * 4 + threadIdx.x * 8;
+            __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_m[threadIdx.x]), rs, at, 0, kCacheSC1);
+            __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_l[threadIdx.x]), rs, at + 4, 0, kCacheSC1);
+        }
     }
 
     __device__ void run(const Args& a, Shared& sh) {
@@ -656,23 +712,42 @@ struct Attention {
                                                    : kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
                 __syncthreads();   // the next piece writes what this one reads
             } else {
-                if (tid < rows) {
-                    const uint32_t at = slot + kRows * DPAD * 4 + tid * 8;
-                    __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_m[tid]), rs, at, 0, kCacheSC1);
-                    __builtin_amdgcn_raw_buffer_store_b32(as_u32(sh.row_l[tid]), rs, at + 4, 0, kCacheSC1);
-                }
-                __builtin_amdgcn_s_waitcnt(0);   // this thread's stores acknowledged
-                __syncthreads();                 // ... and every thread's, before the count
+                publish_sums(sh, rs, slot, rows);
                 const int w0 = base / run, pieces = (base + span.units - 1) / run - w0 + 1;
+                const auto piece_slot = [&](int i) {   // a run that starts before this sequence ends with it: its second slot
+                    const int w = w0 + i;
+                    return (uint32_t)(2 * (w * a.groups + h) + (w * run < base ? 1 : 0)) * a.slot_bytes;
+                };
+                const auto final = [&](int row, int d, float4_t sum) { store4(a, b, head0 + row, d, sum, v_by / sh.row_l[row]); };
                 uint32_t* counter = a.counters + (b * a.groups + h) * kCounterStep;
-                if (tid == 0)
-                    sh.last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                              (uint32_t)(pieces - 1);
-                __syncthreads();
-                if (uniform(sh.last)) {
-                    join(a, sh, rs, w0, pieces, run, base, h, rows, b, head0, v_by);
-                    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                bool joined = false;
+                if (pieces <= 2 * kParty) {
+                    if (arrive(sh, counter, pieces)) {
+                        join(a, sh, rs, pieces, rows, piece_slot, final);
+                        joined = true;
+                    }
+                } else {   // in two steps, the first of them by many workgroups side by side; a party's sum replaces its first piece
+                    const int party = (which - w0) / kParty, parties = (pieces + kParty - 1) / kParty;
+                    const int members = pieces - party * kParty < kParty ? pieces - party * kParty : kParty;
+                    if (arrive(sh, counter + 1 + party, members)) {
+                        const uint32_t to = piece_slot(party * kParty);
+                        join(a, sh, rs, members, rows, [&](int i) { return piece_slot(party * kParty + i); },
+                             [&](int row, int d, float4_t sum) { sh.sums[row][d / 4] = sum; });
+                        __syncthreads();   // every piece has been read
+                        for (int x = tid; x < rows * (a.dim / 4); x += 256) {
+                            const int row = x / (a.dim / 4), d = 4 * (x - row * (a.dim / 4));
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uint4_t, sh.sums[row][d / 4]), rs,
+                                                                   to + (uint32_t)(row * DPAD + d) * 4, 0, kCacheSC1);
+                        }
+                        publish_sums(sh, rs, to, rows);
+                        if (arrive(sh, counter, parties)) {
+                            join(a, sh, rs, parties, rows, [&](int i) { return piece_slot(i * kParty); }, final);
+                            joined = true;
+                        }
+                    }
                 }
+                if (joined && a.lse && tid < rows)
+                    a.lse[(int64_t)b * a.heads + head0 + tid] = kLn2 * (sh.row_m[tid] - T::kLift) + logf(sh.row_l[tid]);
                 __syncthreads();
             }
             u += c1 - c0;
@@ -686,9 +761,9 @@ struct Attention {
     }
 };
 
-template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE>
+template <class T, bool E4M3, int PAIRS, int VW, int VB, bool WHOLE, bool LINES>
 __global__ __launch_bounds__(256, PAIRS <= 2 ? 2 : 1) void k_attn(Args a) {
-    using Op = Attention<T, E4M3, PAIRS, VW, VB, WHOLE>;
+    using Op = Attention<T, E4M3, PAIRS, VW, VB, WHOLE, LINES>;
     __shared__ typename Op::Shared sh;
     Op op;
     op.run(a, sh);
@@ -697,17 +772,26 @@ __global__ __launch_bounds__(256, PAIRS <= 2 ? 2 : 1) void k_attn(Args a) {
 typedef void (*Kernel)(Args);
 
 template <class T, bool E4M3, bool WHOLE>
-Kernel pick_dim(int dim) {
-    if (dim <= 64) return k_attn<T, E4M3, 1, 4, 1, WHOLE>;
-    if (dim <= 128) return k_attn<T, E4M3, 2, 8, 1, WHOLE>;
-    if (dim <= 192) return k_attn<T, E4M3, 3, 4, 3, WHOLE>;
-    return k_attn<T, E4M3, 4, 8, 2, WHOLE>;
+Kernel pick_dim(int dim, bool once) {
+    const bool lines = once && dim % (E4M3 ? 128 : 64) == 0;
+    if (dim <= 64) {
+        if constexpr (!E4M3)
+            if (lines) return k_attn<T, E4M3, 1, 4, 1, WHOLE, true>;
+        return k_attn<T, E4M3, 1, 4, 1, WHOLE, false>;
+    }
+    if (dim <= 128) return lines ? k_attn<T, E4M3, 2, 8, 1, WHOLE, true> : k_attn<T, E4M3, 2, 8, 1, WHOLE, false>;
+    if (dim <= 192) {
+        if constexpr (!E4M3)
+            if (lines) return k_attn<T, E4M3, 3, 4, 3, WHOLE, true>;
+        return k_attn<T, E4M3, 3, 4, 3, WHOLE, false>;
+    }
+    return lines ? k_attn<T, E4M3, 4, 8, 2, WHOLE, true> : k_attn<T, E4M3, 4, 8, 2, WHOLE, false>;
 }
 
 template <class T>
-Kernel pick(bool e4m3, bool whole, int dim) {
-    if (e4m3) return whole ? pick_dim<T, true, true>(dim) : pick_dim<T, true, false>(dim);
-    return whole ? pick_dim<T, false, true>(dim) : pick_dim<T, false, false>(dim);
+Kernel pick(bool e4m3, bool whole, int dim, bool once) {
+    if (e4m3) return whole ? pick_dim<T, true, true>(dim, once) : pick_dim<T, true, false>(dim, once);
+    return whole ? pick_dim<T, false, true>(dim, once) : pick_dim<T, false, false>(dim, once);
 }
 
 int padded(int dim) { return (dim + 63) / 64 * 64; }
@@ -797,7 +881,8 @@ extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cac
     a.scale = p.scale;
     a.softcap = p.softcap;
     const bool whole_pages = kv.page_size % 16 == 0, e4m3 = kv.type == SGEMV_E4M3;
-    const Kernel kernel = p.type == SGEMV_F16 ? pick<F16>(e4m3, whole_pages, kv.dim) : pick<BF16>(e4m3, whole_pages, kv.dim);
+    const bool once = a.groups == kv.heads;   // a key head's query heads fit one tile
+    const Kernel kernel = p.type == SGEMV_F16 ? pick<F16>(e4m3, whole_pages, kv.dim, once) : pick<BF16>(e4m3, whole_pages, kv.dim, once);
     // a launch counts its units in 30 bits and its heads by kMaxHeads counters
     const int64_t units = a.capacity / kUnit + 2;
     int64_t per = kMaxHeads / a.groups;
