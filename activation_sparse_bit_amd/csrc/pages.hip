@@ -1,13 +1,15 @@
 // Pages of a cache: sgemv_pages_fork, sgemv_pages_compact, sgemv_pages_copy.
 //
-// Whole numbers and copies.  A fork is two launches (three where the counts go
-// to another array).  The first has a workgroup for each row, which counts the
-// row's children and adds (children - 1) to every page of the row, once for
-// all of them; the last workgroup to arrive then plans: who copies a shared
-// page, how many pages each row needs (a sum over the rows before it), which
-// free pages there are, lowest first.  The second launch writes tables, slots
-// and lengths, and copies.  A compaction counts the used pages of every 4096,
-// then ranks movers and free places with those sums, then renames and copies.
+// Whole numbers and copies.  A fork adds (children - 1) to the count of every
+// page of every row, once for all of a row's children, and then plans: who
+// copies a shared page, how many pages each row needs (a sum over the rows
+// before it), which free pages there are, lowest first.  Where the counts fit
+// one workgroup's LDS, that is one workgroup's work; else a workgroup for each
+// row adds, and the last one to arrive plans (after a launch that copies the
+// counts, where they go to another array).  The last launch writes tables,
+// slots and lengths, and copies.  A compaction counts the used pages of every
+// 4096, then ranks movers and free places with those sums, then renames and
+// copies.
 //
 // Copies are bound by HBM: 16 bytes a lane, every pair, layer, keys and values
 // cut into pieces of 16 KiB over one fixed grid, since only the device knows
@@ -28,6 +30,10 @@ constexpr int kThreads = 256;
 constexpr int kBlock = 4096;               // pages of a block of a compaction
 constexpr int kDeep = 4;                   // vectors of a thread and piece
 constexpr int kPiece = kThreads * kDeep;   // vectors of a piece of a copy
+
+constexpr int kSmallThreads = 1024;        // of a plan in LDS, and its most rows
+constexpr int kSmallPages = 6144;          // 8 bytes of LDS each
+constexpr int kSmallEntries = 1 << 16;     // of its table
 
 // What the kernels copy: one geometry, the addresses of every layer.
 struct Copy {
@@ -78,6 +84,7 @@ __device__ __forceinline__ void poke(int32_t* p, int v) { __hip_atomic_store(p, 
 __device__ __forceinline__ void add(int32_t* p, int v) { __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // Sum over the workgroup's threads before this one; `all` gets the whole sum.
+template <int THREADS = kThreads>
 __device__ __forceinline__ int block_before(int v, int* shared, int& all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int scan = v;
@@ -92,7 +99,7 @@ __device__ __forceinline__ int block_before(int v, int* shared, int& all) {
     int before = scan - v;
     all = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < THREADS / 64; ++w) {
         if (w < wave) before += shared[w];
         all += shared[w];
     }
@@ -114,7 +121,9 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int n, int* shared) {
     return last;
 }
 
-template <class T>
+// ONCE: whole pages, which nobody reads again soon, past the caches (1500 pages of 64 tokens, a quarter of them moved:
+// 97.5 us, 88.4 so; parts of pages that are read next: 26.5, 28.8 so).
+template <bool ONCE, class T>
 __device__ __forceinline__ void copy_piece(const Copy& c, bool keys, uint8_t* base, int source, int target, int tokens, int first) {
     const int64_t page = keys ? c.k_page : c.v_page, token = keys ? c.k_token : c.v_token, head = keys ? c.k_head : c.v_head;
     const uint8_t* from = base + source * page;
@@ -135,15 +144,22 @@ __device__ __forceinline__ void copy_piece(const Copy& c, bool keys, uint8_t* ba
             h = r - t * (int)c.heads.d;
         }
         at[i] = r < rows && t < tokens ? t * token + h * head + piece * (int64_t)sizeof(T) : -1;
-        if (at[i] >= 0) got[i] = *reinterpret_cast<const T*>(from + at[i]);
+        if (at[i] >= 0) {
+            const T* p = reinterpret_cast<const T*>(from + at[i]);
+            got[i] = ONCE ? __builtin_nontemporal_load(p) : *p;
+        }
     }
 #pragma unroll
     for (int i = 0; i < kDeep; ++i)
-        if (at[i] >= 0) *reinterpret_cast<T*>(to + at[i]) = got[i];
+        if (at[i] >= 0) {
+            T* p = reinterpret_cast<T*>(to + at[i]);
+            if (ONCE) __builtin_nontemporal_store(got[i], p);
+            else *p = got[i];
+        }
 }
 
 // Pieces of all pairs over the grid; pair(j, source, target, tokens).
-template <class F>
+template <bool ONCE, class F>
 __device__ __forceinline__ void copy_pairs(const Copy& c, int count, F pair) {
     const int64_t per = (int64_t)c.layers * 2 * c.pieces, all = per * count;
     for (int64_t x = blockIdx.x; x < all; x += gridDim.x) {
@@ -158,8 +174,8 @@ __device__ __forceinline__ void copy_pairs(const Copy& c, int count, F pair) {
         if (tokens > c.page_size) tokens = c.page_size;
         if ((uint32_t)source >= (uint32_t)c.pages || (uint32_t)target >= (uint32_t)c.pages || tokens <= 0 || source == target) continue;
         uint8_t* base = keys ? c.k[layer] : c.v[layer];
-        if (c.wide) copy_piece<uint4_t>(c, keys, base, source, target, tokens, first);
-        else copy_piece<uint2_t>(c, keys, base, source, target, tokens, first);
+        if (c.wide) copy_piece<ONCE, uint4_t>(c, keys, base, source, target, tokens, first);
+        else copy_piece<ONCE, uint2_t>(c, keys, base, source, target, tokens, first);
     }
 }
 
@@ -167,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void k_copy(Copy c, const int32_t* pairs,
     int n = most;
     if (count) n = count[0] < most ? count[0] : most;
     if (n > 0)
-        copy_pairs(c, n, [&](int j, int& source, int& target, int& tokens) {
+        copy_pairs<false>(c, n, [&](int j, int& source, int& target, int& tokens) {
             source = pairs[3 * (int64_t)j];
             target = pairs[3 * (int64_t)j + 1];
             tokens = pairs[3 * (int64_t)j + 2];
@@ -221,13 +237,14 @@ __global__ __launch_bounds__(kThreads) void k_fork(Fork a) {
     }
 
     // the plan: a thread has `each` rows in a row
+    constexpr int kDeepScan = 8;
     const int each = (a.rows + kThreads - 1) / kThreads, r0 = tid * each;
     const int r1 = r0 + each < a.rows ? r0 + each : a.rows;
     if (tid == 0) bad_rows = 0;
     __syncthreads();
     for (int r = r0; r < r1; ++r) {
         int parent;
-        const int length = inherited(a, r, parent), grow = a.grow ? a.grow[r] : 0, at = divide(length, a.page);
+        const int grow = a.grow ? a.grow[r] : 0, length = inherited(a, r, parent), at = divide(length, a.page);
         int id = -1;   // the partly filled last page of a growing row
         if (grow > 0 && at * (int)a.page.d != length) id = a.table[parent * a.ld_table + at];
         if ((uint32_t)id >= (uint32_t)a.pages) id = -1;
@@ -253,32 +270,31 @@ __global__ __launch_bounds__(kThreads) void k_fork(Fork a) {
     const bool bad = bad_rows != 0;
     int need = 0, copied = 0;
     for (int r = r0; r < r1 && !bad; ++r) {
-        const Row row = a.row[r];
-        int copies = 0;   // of a shared page, but the last holder's where all of them grow
-        if (row.start >= 0) {
+        Row row = a.row[r];
+        if (row.start >= 0) {   // a shared page is copied, but by its last holder where all of them grow
             const int32_t* mark = a.mark + 2 * (int64_t)row.start;
             const int held = peek(a.refs_out + row.start);
-            copies = held > 1 && !(peek(mark) == held && peek(mark + 1) == r);
+            row.copied = held > 1 && !(peek(mark) == held && peek(mark + 1) == r);
         }
-        copied += copies;
-        need += copies + parts(row.length + row.grow, a.page) - parts(row.length, a.page);
-        a.row[r].copied = copies;
+        copied += row.copied;
+        need += row.copied + parts(row.length + row.grow, a.page) - parts(row.length, a.page);
+        a.row[r].copied = row.copied;
     }
     int needed, pairs;
     int start = block_before(need, shared, needed);
     int pair = block_before(copied, shared, pairs);
     // the lowest free pages
     int have = 0;
-    constexpr int kDeepScan = 8;
     for (int64_t base = 0; base < a.pages && have < needed; base += kThreads * kDeepScan) {
-        int free_here[kDeepScan], n = 0;
         const int64_t at = base + tid * kDeepScan;
+        int free_here[kDeepScan], n = 0;
+#pragma unroll
+        for (int i = 0; i < kDeepScan; ++i) free_here[i] = peek(a.refs_out + (at + i < a.pages ? at + i : a.pages - 1));
 #pragma unroll
         for (int i = 0; i < kDeepScan; ++i) {
-            free_here[i] = at + i < a.pages ? peek(a.refs_out + at + i) <= 0 : 0;
+            free_here[i] = at + i < a.pages && free_here[i] <= 0;
+            n += free_here[i];
         }
-#pragma unroll
-        for (int i = 0; i < kDeepScan; ++i) n += free_here[i];
         int all, rank = have + block_before(n, shared, all);
 #pragma unroll
         for (int i = 0; i < kDeepScan; ++i)
@@ -296,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void k_fork(Fork a) {
         a.count[0] = grows ? pairs : 0;
     }
     __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();   // free_list, by this workgroup's other threads
+    __syncthreads();   // the fresh pages, by this workgroup's other threads
     for (int r = r0; r < r1; ++r) {
         Row row = a.row[r];
         const int id = row.start;
@@ -322,7 +338,110 @@ __global__ __launch_bounds__(kThreads) void k_fork(Fork a) {
         for (int k = 0; k < 3; ++k) a.pairs[3 * (int64_t)i + k] = -1;
 }
 
+// The same by one workgroup, a thread for each row, with the counts in LDS (and beside them a word for every page: how many
+// growing rows have it, and the highest of them plus one).
+__global__ __launch_bounds__(kSmallThreads) void k_fork_small(Fork a, SgemvDiv width) {
+    extern __shared__ int counts[];
+    __shared__ int shared[kSmallThreads / 64], children[kSmallThreads], lengths[kSmallThreads], parents[kSmallThreads];
+    __shared__ int bad_rows;
+    uint32_t* mark = reinterpret_cast<uint32_t*>(counts + a.pages);
+    const int tid = threadIdx.x;
+    const bool is_row = tid < a.rows;
+    for (int i = tid; i < a.pages; i += kSmallThreads) counts[i] = a.refs[i];
+    int parent = tid, grow = 0, own = 0;
+    if (is_row) {
+        if (a.parents) parent = a.parents[tid];
+        if (a.grow) grow = a.grow[tid];
+        own = length_of(a, tid);
+    }
+    children[tid] = 0;
+    lengths[tid] = own;
+    if (tid == 0) bad_rows = 0;
+    __syncthreads();
+    const bool alive = is_row && (uint32_t)parent < (uint32_t)a.rows;
+    const int length = alive ? lengths[parent] : 0;
+    parents[tid] = alive ? parent : tid;
+    if (alive) atomicAdd(&children[parent], 1);
+    const int at = divide(length, a.page);
+    int id = -1;   // the partly filled last page of a growing row
+    if (grow > 0 && at * (int)a.page.d != length) id = a.table[parent * a.ld_table + at];
+    if ((uint32_t)id >= (uint32_t)a.pages) id = -1;
+    if (is_row && (grow < 0 || (a.slots && grow > a.max_grow) || (int64_t)length + grow > (int64_t)a.max_pages * (int)a.page.d))
+        atomicAdd(&bad_rows, 1);
+    if (id >= 0) mark[id] = 0;
+    __syncthreads();
+    if (a.parents) {
+        constexpr int kDeepRows = 4;
+        const int all = a.rows * a.max_pages;
+        for (int x0 = tid; x0 < all; x0 += kSmallThreads * kDeepRows) {
+            int own_id[kDeepRows], more[kDeepRows], taken[kDeepRows];
+#pragma unroll
+            for (int i = 0; i < kDeepRows; ++i) {
+                const int x = x0 + i * kSmallThreads, r = x < all ? divide(x, width) : 0, c = x - r * a.max_pages;
+                more[i] = x < all && c < parts(lengths[r], a.page) ? children[r] - 1 : 0;
+                own_id[i] = more[i] ? a.table[r * a.ld_table + c] : -1;
+                if (a.staged && x < all) taken[i] = a.table[parents[r] * a.ld_table + c];
+            }
+#pragma unroll
+            for (int i = 0; i < kDeepRows; ++i) {
+                if ((uint32_t)own_id[i] < (uint32_t)a.pages) atomicAdd(&counts[own_id[i]], more[i]);
+                if (a.staged && x0 + i * kSmallThreads < all) a.staged[x0 + i * kSmallThreads] = taken[i];
+            }
+        }
+    }
+    if (id >= 0) atomicAdd(&mark[id], 1u << 16);
+    __syncthreads();
+    if (id >= 0) atomicMax(&mark[id], (mark[id] & 0xFFFF0000u) | (uint32_t)(tid + 1));
+    __syncthreads();
+    const bool bad = bad_rows != 0;
+    int copied = 0, need = 0;
+    if (is_row && !bad) {
+        if (id >= 0) copied = counts[id] > 1 && !((int)(mark[id] >> 16) == counts[id] && (int)(mark[id] & 0xFFFFu) == tid + 1);
+        need = copied + parts(length + grow, a.page) - parts(length, a.page);
+    }
+    int needed, pairs, have = 0;
+    const int start = block_before<kSmallThreads>(need, shared, needed);
+    const int pair = block_before<kSmallThreads>(copied, shared, pairs);
+    for (int base = 0; base < a.pages && have < needed; base += kSmallThreads) {
+        const bool is_free = base + tid < a.pages && counts[base + tid] <= 0;
+        int all;
+        const int rank = have + block_before<kSmallThreads>(is_free, shared, all);
+        if (is_free && rank < needed) a.free_list[rank] = base + tid;
+        have += all;
+    }
+    const int missing = needed > have ? needed - have : 0;
+    const bool grows = !bad && missing == 0;
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();   // the fresh pages, by other threads; the counts have been read
+    if (is_row) {
+        if (grows) {
+            for (int i = 0; i < need; ++i) counts[a.free_list[start + i]] = 1;
+            if (copied) {
+                atomicSub(&counts[id], 1);
+                a.pairs[3 * pair] = id;
+                a.pairs[3 * pair + 1] = a.free_list[start];
+                a.pairs[3 * pair + 2] = length - at * (int)a.page.d;
+            }
+        }
+        a.row[tid] = grows ? Row{length, grow, start, copied} : Row{length, 0, 0, 0};
+    }
+    const int listed = grows ? pairs : 0;
+    for (int i = 3 * listed + tid; i < 3 * a.rows; i += kSmallThreads) a.pairs[i] = -1;
+    if (tid == 0) {
+        a.status[0] = missing;
+        a.status[1] = bad_rows;
+        a.count[0] = listed;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.pages; i += kSmallThreads) a.refs_out[i] = counts[i];
+}
+
 __global__ __launch_bounds__(kThreads) void k_fork_write(Fork a, Copy c) {
+    copy_pairs<false>(c, a.count[0], [&](int j, int& source, int& target, int& tokens) {
+        source = a.pairs[3 * (int64_t)j];
+        target = a.pairs[3 * (int64_t)j + 1];
+        tokens = a.pairs[3 * (int64_t)j + 2];
+    });
     const int64_t stride = (int64_t)gridDim.x * kThreads, from = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const auto entry = [&](int r, const Row& row, int col) {
         const int used = parts(row.length, a.page);
@@ -351,21 +470,25 @@ __global__ __launch_bounds__(kThreads) void k_fork_write(Fork a, Copy c) {
             }
             a.slots[x] = slot;
         }
-    copy_pairs(c, a.count[0], [&](int j, int& source, int& target, int& tokens) {
-        source = a.pairs[3 * (int64_t)j];
-        target = a.pairs[3 * (int64_t)j + 1];
-        tokens = a.pairs[3 * (int64_t)j + 2];
-    });
+}
+
+// Used pages from x on, below end and in x's block: this thread's share.  Loads without a branch are in flight at once.
+__device__ __forceinline__ int used_in(const Compact& a, int x, int end) {
+    int held[kBlock / kThreads], n = 0;
+#pragma unroll
+    for (int i = 0; i < kBlock / kThreads; ++i) {
+        const int at = x + (int)threadIdx.x + i * kThreads;
+        held[i] = a.refs[at < end ? at : end - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kBlock / kThreads; ++i) n += x + (int)threadIdx.x + i * kThreads < end && held[i] > 0;
+    return n;
 }
 
 __global__ __launch_bounds__(kThreads) void k_count_used(Compact a) {
     __shared__ int shared[kThreads / 64];
     const int tid = threadIdx.x;
-    int n = 0;
-    for (int i = tid; i < kBlock; i += kThreads) {
-        const int64_t x = (int64_t)blockIdx.x * kBlock + i;
-        n += x < a.pages && a.refs[x] > 0;
-    }
+    const int n = used_in(a, blockIdx.x * kBlock, a.pages);
     int all;
     block_before(n, shared, all);
     if (tid == 0) poke(a.before + blockIdx.x, all);
@@ -380,31 +503,28 @@ __global__ __launch_bounds__(kThreads) void k_count_used(Compact a) {
     if (tid == 0) poke(a.before + a.blocks, sum);
 }
 
-// Used pages of [0, x) for x in block b, by the whole workgroup.
-__device__ __forceinline__ int used_before(const Compact& a, int x, int* shared) {
-    const int b = x / kBlock;
-    int n = 0;
-    for (int i = b * kBlock + threadIdx.x; i < x; i += kThreads) n += a.refs[i] > 0;
-    int all;
-    block_before(n, shared, all);
-    return a.before[b] + all;
-}
-
 __global__ __launch_bounds__(kThreads) void k_rank(Compact a) {
     __shared__ int shared[kThreads / 64];
     const int tid = threadIdx.x;
-    const int used = a.before[a.blocks];
-    const int stay = used < a.pages ? used_before(a, used, shared) : used;   // used pages below `used`
     constexpr int kEach = kBlock / kThreads;
     const int64_t at = (int64_t)blockIdx.x * kBlock + tid * kEach;
+    int held[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) held[i] = a.refs[at + i < a.pages ? at + i : a.pages - 1];
+    const int used = a.before[a.blocks], edge = used / kBlock * kBlock;   // the block that the border is in
+    int all, stay = used;                                                // used pages below `used`
+    if (used < a.pages) {
+        block_before(used > edge ? used_in(a, edge, used) : 0, shared, all);
+        stay = a.before[edge / kBlock] + all;
+    }
     bool in_use[kEach];
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        in_use[i] = at + i < a.pages && a.refs[at + i] > 0;
+        in_use[i] = at + i < a.pages && held[i] > 0;
         n += in_use[i];
     }
-    int all, before = a.before[blockIdx.x] + block_before(n, shared, all);
+    int before = a.before[blockIdx.x] + block_before(n, shared, all);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int64_t x = at + i;
@@ -455,7 +575,7 @@ __global__ __launch_bounds__(kThreads) void k_compact_write(Compact a, Copy c) {
             if ((held > 0) == (x < used)) a.refs_out[x] = held;
         }
     }
-    copy_pairs(c, moves, [&](int j, int& source, int& target, int& tokens) {
+    copy_pairs<true>(c, moves, [&](int j, int& source, int& target, int& tokens) {
         source = a.source[j];
         target = a.target[j];
         tokens = (int)a.page.d;
@@ -601,12 +721,20 @@ extern "C" int sgemv_pages_fork(const sgemv_pages_args* args, const sgemv_kv* ca
     a.ld_table = p.ld_table; a.ld_table_out = p.ld_table_out;
     a.page = sgemv_div(p.page_size);
     a.rows = p.rows; a.max_pages = p.max_pages; a.pages = p.pages; a.max_grow = p.max_grow;
-    if (p.refs_out != p.refs) {
-        void* kargs[] = {(void*)&a.refs, &a.refs_out, &a.pages};
-        if (int e = launch(reinterpret_cast<const void*>(k_move), (unsigned)((p.pages + kThreads - 1) / kThreads), kargs, stream)) return e;
+    if (p.rows <= kSmallThreads && p.pages <= kSmallPages && (int64_t)p.rows * p.max_pages <= kSmallEntries) {
+        SgemvDiv width = sgemv_div(p.max_pages);
+        void* plan[] = {&a, &width};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k_fork_small), dim3(1), dim3(kSmallThreads), plan,
+                                             (size_t)p.pages * 8, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return sgemv_hip_failed((int)e);
+    } else {
+        if (p.refs_out != p.refs) {
+            void* kargs[] = {(void*)&a.refs, &a.refs_out, &a.pages};
+            if (int e = launch(reinterpret_cast<const void*>(k_move), (unsigned)((p.pages + kThreads - 1) / kThreads), kargs, stream)) return e;
+        }
+        void* plan[] = {&a};
+        if (int e = launch(reinterpret_cast<const void*>(k_fork), a.parents ? (unsigned)p.rows : 1u, plan, stream)) return e;
     }
-    void* plan[] = {&a};
-    if (int e = launch(reinterpret_cast<const void*>(k_fork), a.parents ? (unsigned)p.rows : 1u, plan, stream)) return e;
     void* write[] = {&a, &c};
     return launch(reinterpret_cast<const void*>(k_fork_write),
                   grid_for((int64_t)p.rows * p.max_pages, (int64_t)p.rows * c.layers * 2 * c.pieces), write, stream);

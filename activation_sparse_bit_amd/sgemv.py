@@ -963,20 +963,30 @@ def _heads_of(t, what: str, code: int, like=None):
 
 
 def _ints(t, what: str, *shape) -> int:
-    """Address of a contiguous int32 tensor of `shape` (None: any size)."""
+    """Address of a contiguous int32 tensor of `shape`."""
+    try:
+        if t.dtype is _torch.int32 and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype is not _torch.int32:
         raise ValueError(f"{what}: dtype {str(t.dtype).replace('torch.', '')}, expected int32")
-    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {''.join('[any]' if n is None else f'[{n}]' for n in shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {''.join(f'[{n}]' for n in shape)}")
+    raise ValueError(f"{what}: must be contiguous")
 
 
 def _table_of(t, what: str, rows: int):
     """(address, row stride, columns) of an int32 [rows][max_pages] table."""
+    try:
+        if t.dtype is _torch.int32 and t.is_contiguous():
+            n, columns = t.shape
+            if n == rows:
+                return t.data_ptr(), columns, columns
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     if t.dtype is not _torch.int32:
@@ -1163,12 +1173,16 @@ def _pages_call(name, table, lengths, refs, table_out, lengths_out, refs_out, wo
     op, ld_out, columns_out = _table_of(table_out, "table_out", rows)
     if columns_out != columns:
         raise ValueError(f"table_out: {columns_out} columns, table has {columns}")
-    lp, rp = _ints(lengths, "lengths", rows), _ints(refs, "refs", None)
+    if not isinstance(refs, _torch.Tensor) or refs.dim() != 1:
+        raise ValueError("refs: expected int32 [pages]")
     pages = refs.shape[0]
+    if slots is not None and (not isinstance(slots, _torch.Tensor) or slots.dim() != 2):
+        raise ValueError(f"slots: expected int32 [{rows}][most]")
+    lp, rp = _ints(lengths, "lengths", rows), _ints(refs, "refs", pages)
     fork = name == "sgemv_pages_fork"
     at = [tp, lp, rp, op, _ints(lengths_out, "lengths_out", rows) if fork else 0, _ints(refs_out, "refs_out", pages),
           0 if parents is None else _ints(parents, "parents", rows), 0 if grow is None else _ints(grow, "grow", rows),
-          0 if slots is None else _ints(slots, "slots", rows, None), _ints(pairs, "pairs", rows if fork else pages, 3),
+          0 if slots is None else _ints(slots, "slots", rows, slots.shape[1]), _ints(pairs, "pairs", rows if fork else pages, 3),
           _ints(count, "count", 1), _ints(status, "status", 2) if fork else 0]
     wp, size = _space(workspace)
     max_grow = 0 if slots is None else slots.shape[1]
@@ -1214,7 +1228,9 @@ def sgemv_pages_copy(caches, pairs, count=None, stream=None):
     caches, packed = _caches(caches)
     if not caches:
         raise ValueError("caches: at least one")
-    pp, cp = _ints(pairs, "pairs", None, 3), 0 if count is None else _ints(count, "count", 1)
+    if not isinstance(pairs, _torch.Tensor) or pairs.dim() != 2:
+        raise ValueError("pairs: expected int32 [n][3]")
+    pp, cp = _ints(pairs, "pairs", pairs.shape[0], 3), 0 if count is None else _ints(count, "count", 1)
     _fits_int32("sgemv_pages_copy", pairs=pairs.shape[0])
     device = caches[0].device
     _on_one_gpu(device, ("caches",) * len(caches) + ("pairs", "count"), tuple(c.k for c in caches) + (pairs, count))
