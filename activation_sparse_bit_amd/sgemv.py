@@ -902,6 +902,9 @@ _BEAM = struct.Struct("@7PN2q6i")
 _PAGES = struct.Struct("@13PN2q6i")
 
 
+_NO_SECTIONS = (0,) * SGEMV_MAX_AXES
+
+
 class KVCache:
     """One layer's paged cache over the caller's tensors: k and v are
     [pages][page_size][heads][dim] in float16, bfloat16 or float8_e4m3fn, any
@@ -1049,23 +1052,25 @@ def sgemv_rotary(q, q_out, positions, inv_freq, *, k=None, k_out=None, v=None, c
         if v is not None:
             at[4], strides[8], strides[9] = _heads_of(v, "v", code, k.shape)
         at[7] = _ints(slots, "slots", tokens)
-    if not isinstance(positions, _torch.Tensor) or positions.dtype is not _torch.int32 or positions.dim() not in (1, 2) \
-            or positions.shape[-1] != tokens or (tokens > 1 and positions.stride(-1) != 1):
+    shape = getattr(positions, "shape", ())
+    if len(shape) not in (1, 2) or positions.dtype is not _torch.int32 or shape[-1] != tokens \
+            or (tokens > 1 and positions.stride(-1) != 1):
         raise ValueError(f"positions: expected int32 [{tokens}] or [axes][{tokens}], the last dimension contiguous")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    at[5], strides[10] = positions.data_ptr(), max(positions.stride(0), tokens) if axes == 1 else positions.stride(0)
-    if _type_code(inv_freq, "inv_freq") != SGEMV_F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    axes = 1 if len(shape) == 1 else shape[0]
+    at[5], strides[10] = positions.data_ptr(), tokens if axes == 1 else positions.stride(0)
+    shape = getattr(inv_freq, "shape", ())
+    if len(shape) != 1 or inv_freq.dtype is not _torch.float32 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq: expected float32 [pairs], contiguous")
-    at[6], pairs = inv_freq.data_ptr(), inv_freq.shape[0]
-    sections = [pairs] if sections is None else list(sections)
-    if len(sections) != axes or axes > SGEMV_MAX_AXES or sum(sections) != pairs or min(sections, default=-1) < 0:
+    at[6], pairs = inv_freq.data_ptr(), shape[0]
+    sections = (pairs,) if sections is None else tuple(sections)
+    if len(sections) != axes or axes > SGEMV_MAX_AXES or sum(sections) != pairs or min(sections) < 0:
         raise ValueError(f"sections: {sections}, expected {axes} numbers that sum to {pairs} (up to {SGEMV_MAX_AXES})")
     _fits_int32("sgemv_rotary", tokens=tokens)
     device = first.device
     _on_one_gpu(device, ("q", "q_out", "k", "k_out", "v", "positions", "inv_freq", "slots", "cache"),
                 (q, q_out, k, k_out, v, positions, inv_freq, slots, None if cache is None else cache.k))
     args = _ROTARY.pack(*at, *strides, tokens, code, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim,
-                        pairs, axes, *sections, *[0] * (SGEMV_MAX_AXES - axes),
+                        pairs, axes, *sections, *_NO_SECTIONS[axes:],
                         (SGEMV_ROTARY_ADJACENT if adjacent else 0) | (SGEMV_ROTARY_STRIPED if striped else 0), scale)
     _call(lib().sgemv_rotary, device, (args, None if cache is None else cache.args, _stream_on(device, stream)),
           "sgemv_rotary")

@@ -241,3 +241,30 @@ def test_graph():
         for name, x in {"table": t, "lengths": n, "refs": r, "slots": slots, "pairs": pairs}.items():
             assert np.array_equal(x.cpu().numpy(), want[name]), (step, name)
         p.check_copies(before, want["pairs"][:want["count"]].tolist())
+
+
+@pytest.mark.parametrize("rows,width,page,spare", [(1025, 4, 3, None), (5, 6, 4, 7000), (40, 1700, 1, None), (8192, 3, 2, None)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_forks_past_one_workgroup(rows, width, page, spare, in_place):
+    """More rows, pages or table entries than one workgroup plans in its LDS."""
+    p = Pool(rows, rows, width, page, spare=spare, heads=1, dim=8, layers=1)
+    for step in range(3):
+        p.fork(p.rng.integers(-1, rows, rows) if step != 1 else None, p.rng.integers(0, 3, rows) if step else None, in_place=in_place)
+    p.fork([rows - 1] * rows, [1] * rows, in_place=in_place)   # all from one, where it fits
+
+
+def test_tables_and_slots_with_strides():
+    """A table whose rows lie apart, in place, with the places behind its rows kept."""
+    p = Pool(9, 5, 6, 8)
+    wide = torch.full((5, 11), 5, dtype=torch.int32, device=DEV)
+    wide[:, :6] = torch.from_numpy(p.table).to(DEV)
+    _, n, r, par, grow = p.dev(p.table, p.lengths, p.refs, [4, 3, 2, 1, 1], [2, 1, 0, 1, 1])
+    e = lambda *s: torch.full(s, 99, dtype=torch.int32, device=DEV)  # noqa: E731
+    slots, pairs, count, status = e(5, 2), e(5, 3), e(1), e(2)
+    want = oracle.pages_fork(p.table, p.lengths, p.refs, 8, [4, 3, 2, 1, 1], [2, 1, 0, 1, 1], 2)
+    t = wide[:, :6]
+    p.lib.sgemv_pages_fork(t, n, r, t, n, r, p.workspace, page_size=8, parents=par, grow=grow, slots=slots, pairs=pairs,
+                           count=count, status=status, caches=p.caches)
+    for name, x in {"table": t, "lengths": n, "refs": r, "slots": slots, "pairs": pairs}.items():
+        assert np.array_equal(x.cpu().numpy(), want[name]), name
+    assert (wide[:, 6:] == 5).all()
