@@ -36,6 +36,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxBatch = 2048;        // entries of one launch
 constexpr int kMostTied = 6 * kThreads; // a part's values to be ranked, before their places tell them apart
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kFar = 67108864.0f;    // 2^26: as far from zero a float may be off from v L by 2, and ever more beyond
 constexpr int kCounterStep = 16;       // words between arrival counters
 constexpr size_t kCounterBytes = (size_t)kMaxBatch * kCounterStep * 4;
 
@@ -277,7 +278,7 @@ template <int TYPE, int RUNS, int N>
 __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
     extern __shared__ uint64_t lds[];
     __shared__ float part_m[kThreads / 64], part_s[kThreads / 64], part_t[kThreads / 64];
-    __shared__ double offset[SGEMV_MAX_BEAMS];
+    __shared__ double offset[SGEMV_MAX_BEAMS], largest[SGEMV_MAX_BEAMS];   // s = (logit - largest) + offset
     __shared__ uint32_t left, bounds[kThreads / 64], wave_bound[kThreads / 64], order[N];
     __shared__ uint64_t part_bound;
     __shared__ Candidate bound;
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
             least = w < full ? fminf(least, part_t[w]) : least;
         }
         // 2^(v L - c), c the largest v L as a float: one rounding each, and none of the largest logit's own
-        float c = m == -INFINITY ? 0.0f : m * kLog2e, sum = 0.0f;
+        const float c = m == -INFINITY ? 0.0f : m * kLog2e;
+        float sum = 0.0f;
 #pragma unroll
         for (int r = 0; r < RUNS; ++r)
 #pragma unroll
@@ -368,7 +370,9 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
         sum = part_s[0];
 #pragma unroll
         for (int w = 1; w < kThreads / 64; ++w) sum += part_s[w];
-        if (sum != sum) {   // the same in every thread: NaN among the logits is left out, an infinity stays
+        if (sum != sum || !(fabsf(c) <= kFar)) {
+            // the same in every thread: NaN among the logits is left out, an infinity stays; and far from zero, where
+            // logits are whole numbers, differences are taken first
             m = -INFINITY;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r)
@@ -381,13 +385,15 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
             m = part_m[0];
 #pragma unroll
             for (int w = 1; w < kThreads / 64; ++w) m = fmaxf(m, part_m[w]);
-            c = m == -INFINITY ? 0.0f : m * kLog2e;
+            const float near = m == -INFINITY ? 0.0f : m * kLog2e;
+            const bool far = !(fabsf(near) <= kFar);
             sum = 0.0f;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (v[r][j] == v[r][j]) sum += __builtin_amdgcn_exp2f(fmaf(v[r][j], kLog2e, -c));
+                    if (v[r][j] == v[r][j])
+                        sum += __builtin_amdgcn_exp2f(far ? (v[r][j] - m) * kLog2e : fmaf(v[r][j], kLog2e, -near));
             sum = wave_sum(sum);
             if (lane == 0) part_s[wave] = sum;
             __syncthreads();
@@ -480,7 +486,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
             if (rank < n && (tid & (per - 1)) == 0) publish(mine + rank, key);
         }
         if (tid >= count && tid < n) publish(mine + tid, 0ull);
-        if (tid == 0) publish(mine + n, (uint64_t)as_u32(m == -INFINITY ? m : c) << 32 | as_u32(sum));
+        if (tid == 0) publish(mine + n, (uint64_t)as_u32(m) << 32 | as_u32(sum));
     }
 
     // the last workgroup of this entry goes on
@@ -506,21 +512,28 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
         const int w = w0 + tid / 16;
         if (w < a.beams) {
             double off = (double)a.scores[entry * a.beams + w];
+            float m = -INFINITY;
             if (!ended(w)) {
-                float m = -INFINITY;
                 for (int p = tid & 15; p < a.parts; p += 16) m = fmaxf(m, __builtin_bit_cast(float, (uint32_t)(lds[w * a.parts + p] >> 32)));
                 m = row_max(m);
                 double s = 0.0;
                 for (int p = tid & 15; p < a.parts; p += 16) {
                     const uint64_t ms = lds[w * a.parts + p];
                     const float pm = __builtin_bit_cast(float, (uint32_t)(ms >> 32)), ps = __builtin_bit_cast(float, (uint32_t)ms);
-                    if (pm > -INFINITY) s += (double)(ps * __builtin_amdgcn_exp2f(pm - m));
+                    if (pm > -INFINITY) {   // what the part's exponents were taken from
+                        const float c = pm * kLog2e;
+                        const double from = fabsf(c) <= kFar ? (double)c : (double)pm * (double)kLog2e;
+                        s += (double)(ps * __builtin_amdgcn_exp2f((float)(from - (double)m * (double)kLog2e)));
+                    }
                 }
                 s = row_sum(s);
                 // back by the factor that the exponents were taken with; not finite where no logit or an infinite one is there
-                off -= ((double)m + log2(s)) / (double)kLog2e;
+                off -= log2(s) / (double)kLog2e;
             }
-            if ((tid & 15) == 0) offset[w] = off;
+            if ((tid & 15) == 0) {
+                offset[w] = off;
+                largest[w] = (double)m;
+            }
         }
     }
     __syncthreads();
@@ -536,7 +549,7 @@ __global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
             if (i == 0 && list == w * a.parts) c = Candidate{key_of(off), (uint64_t)(63 - w) << 52 | (0xFFFFFu - (uint32_t)a.end_token)};
             return c;
         }
-        if (key) c = Candidate{key_of((double)value_of<TYPE>((uint32_t)(key >> 32)) + off), place_of(w, key)};
+        if (key) c = Candidate{key_of(((double)value_of<TYPE>((uint32_t)(key >> 32)) - largest[w]) + off), place_of(w, key)};
         return c;
     };
     const auto kth = [&](int list, int i) { return fetch(records + (int64_t)list * record + i); };

@@ -98,10 +98,10 @@ def beam_select(logits, scores, choices, finished=None, end_token=0):
         m = x.max()
         if not np.isfinite(m):
             continue
-        off = m + math.log(np.exp(x - m).sum())
+        off = math.log(np.exp(x - m).sum())
         there = np.nonzero(x > -np.inf)[0]
         first = there[np.lexsort((there, -x[there]))][:choices + 1]   # of one beam no more can be chosen
-        found += [(-(s + (float(x[v]) - off)), w, -float(x[v]), int(v)) for v in first]
+        found += [(-(s + ((float(x[v]) - m) - off)), w, -float(x[v]), int(v)) for v in first]
     found.sort()
     best = found[:choices]
     fill = choices - len(best)

@@ -174,3 +174,23 @@ def test_repeats_graph_and_shared_workspace():
             assert torch.equal(x, y)
         for x, y in zip(want_a, out):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fill", [-1e9, -1e10, -1e30, "lowest", 1e9, 1e30, "half of the largest"])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_logits_far_from_zero(fill, x):
+    """Beams, and whole parts of a vocabulary, that hold one value far from zero, as masks leave them."""
+    big = torch.finfo(T[x]).max
+    fill = {"lowest": -big, "half of the largest": big / 2}.get(fill, fill)
+    _, scores = problem(10, 3, 4, 1, x)
+    logits = torch.full((3, 4, 30001), fill, device=DEV).to(T[x])
+    check(logits, scores, 9)                                     # every beam even
+    some = logits.clone()
+    g = torch.Generator().manual_seed(11)
+    some[:, :, ::4001] = torch.randn(3, 4, 8, generator=g).to(T[x]).to(DEV)
+    check(some, scores, 9)                                       # few others, here and there
+    some[:, 2:] = logits[:, 2:]
+    some[0, 1, 100:200] = float("-inf")
+    some[1, 2, 5] = float("nan")
+    some[1, 3, 29000:] = -big
+    check(some, scores, 40)
