@@ -273,9 +273,10 @@ __device__ __forceinline__ void finish(const Args& a, Candidate* found, int ther
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// RUNS runs of eight values a thread, at most N choices.
+// RUNS runs of eight values a thread, at most N choices.  Six workgroups a compute unit hide each other's waits (48 x 8 x
+// 100003: 33.9 us, five 36.3, eight 34); with 64 choices that would spill more.
 template <int TYPE, int RUNS, int N>
-__global__ __launch_bounds__(kThreads, 5) void k_beam(Args a) {
+__global__ __launch_bounds__(kThreads, N <= 16 ? 6 : 5) void k_beam(Args a) {
     extern __shared__ uint64_t lds[];
     __shared__ float part_m[kThreads / 64], part_s[kThreads / 64], part_t[kThreads / 64];
     __shared__ double offset[SGEMV_MAX_BEAMS], largest[SGEMV_MAX_BEAMS];   // s = (logit - largest) + offset
