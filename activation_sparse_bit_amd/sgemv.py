@@ -1100,6 +1100,8 @@ def sgemv_attn_paged(q, cache: KVCache, table, lengths, out, workspace, *, scale
         raise ValueError(f"cache: {cache.heads} heads of {cache.dim}, q has {heads} of {dim}")
     if cache.type not in (code, SGEMV_E4M3):
         raise ValueError("cache: must have q's type, or float8_e4m3fn")
+    if softcap and not softcap >= 2.0 ** -126:   # smaller ones would be none as a float
+        raise ValueError(f"softcap: {softcap}, expected 0 or a normal float above it")
     tp, ld, columns = _table_of(table, "table", batch)
     lp, zp = _ints(lengths, "lengths", batch), 0
     if lse is not None:

@@ -708,7 +708,7 @@ typedef struct sgemv_attn_args {
     int32_t        max_pages;
     int32_t        window;     /* the last `window` tokens are seen; 0: all      */
     float          scale;      /* finite                                         */
-    float          softcap;    /* >= 0; 0: none                                  */
+    float          softcap;    /* 0: none; else a normal number above it         */
     int32_t        reserved;   /* 0                                              */
 } sgemv_attn_args;
 
@@ -765,15 +765,17 @@ typedef struct sgemv_beam_args {
  * sgemv_beam_select - the best continuations of a batch of beam searches:
  *   s(w, v) = scores[w] + logits[w][v] - log sum_u exp logits[w][u]
  * the `choices` largest over beams w and tokens v, largest first, equal ones by
- * the lowest w, then the largest logit, then the lowest v.  A beam with finished != 0 has one candidate,
- * end_token, at its own score.  Candidates are those with a finite s: a logit of
- * -infinity or NaN is none, a beam whose score or whose sum of exponentials is
- * not finite (or 0) has none.  Where there are fewer than `choices`, the rest
- * are token -1, parent -1, score -infinity.  s is formed and compared in 64
- * bits, from fp32 exponentials, and rounded to fp32 at the end.  `parents` is what sgemv_pages_fork takes (as row
+ * the lowest w, then the largest logit, then the lowest v.  A beam with
+ * finished != 0 has one candidate, end_token, at its own score.  A logit of
+ * -infinity or NaN is no candidate; a beam whose score is not finite, whose
+ * logits are all none, or one of whose logits is +infinity, has none.  Where
+ * there are fewer than `choices`, the rest are token -1, parent -1, score
+ * -infinity.  s is formed and compared in 64 bits, from fp32 exponentials, and
+ * rounded to fp32 at the end.  `parents` is what sgemv_pages_fork takes (as row
  * batch * beams + parent).
- * EINVAL for NULL, a bad type or end_token; ESIZE for sizes, strides, too small
- * a workspace (sgemv_beam_workspace_bytes); EALIGN for pointers.
+ * EINVAL for NULL, a bad type or end_token, an overlap; ESIZE for sizes,
+ * strides, too small a workspace (sgemv_beam_workspace_bytes); EALIGN for
+ * pointers.
  */
 int sgemv_beam_select(const sgemv_beam_args* a, void* stream);
 
@@ -792,7 +794,8 @@ typedef struct sgemv_pages_args {
     int32_t*       refs_out;
     const int32_t* parents;      /* fork: device [rows], or NULL: each its own    */
     const int32_t* grow;         /* fork: device [rows], or NULL: none           */
-    int32_t*       slots;        /* fork: device [rows][max_grow], or NULL        */
+    int32_t*       slots;        /* fork: device [rows][max_grow], or NULL; not
+                                    used where max_grow is 0                     */
     int32_t*       pairs;        /* device [rows][3] (fork) or [pages][3]
                                     (compact): source, target, tokens            */
     int32_t*       count;        /* device [1]: pairs in use; the rest are -1     */

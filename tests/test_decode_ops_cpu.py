@@ -144,6 +144,8 @@ def test_attention_refusals():
     refused(attn(lse=z(3, 2)), "lse")
     refused(attn(cache=None), "KVCache")
     refused(attn(window=1 << 40), "window")
+    refused(attn(softcap=1e-60), "softcap")
+    refused(attn(softcap=-1.0), "softcap")
 
 
 def rot(**kw):
@@ -264,7 +266,7 @@ def test_library_refuses_attention():
                 out_head=64, ld=2, t=0, batch=2, heads=4, pages=2, window=0, scale=1.0, cap=0.0, reserved=0)
     at = lambda **kw: status("sgemv_attn_paged", sgemv._ATTN.pack(*{**base, **kw}.values()), kv())  # noqa: E731
     for kw in (dict(q=0), dict(out=0), dict(table=0), dict(lengths=0), dict(ws=0), dict(t=2), dict(reserved=1), dict(scale=math.inf),
-               dict(scale=math.nan), dict(cap=-1.0), dict(cap=math.inf), dict(heads=5), dict(out=A + 64), dict(out=3 * A + 32),
+               dict(scale=math.nan), dict(cap=-1.0), dict(cap=math.inf), dict(cap=math.nan), dict(cap=1e-40), dict(heads=5), dict(out=A + 64), dict(out=3 * A + 32),
                dict(lse=4 * A + 4), dict(out=7 * A), dict(lse=A)):
         assert at(**kw) == sgemv.SGEMV_EINVAL, kw
     for kw in (dict(batch=-1), dict(heads=0), dict(heads=2000), dict(pages=0), dict(ld=1), dict(window=-1), dict(size=1000),
