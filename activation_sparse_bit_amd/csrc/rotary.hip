@@ -10,8 +10,8 @@
 // turn that is left.
 //
 // Nothing is computed on the way that a stream of q, k and v does not hide:
-// bound by HBM for a prompt (16384 tokens, 64 + 16 heads of 128 with three axes:
-// 124 us for 671 MB read and written, 5.4 TB/s, a plain copy reaches 5.2 to
+// bound by HBM for a prompt (16384 tokens, 64 query and 8 key heads of 128, three
+// axes: 124 us for 671 MB read and written, 5.4 TB/s, where a copy reaches 5.2 to
 // 5.7), by the launch for a token (4.3 us).  One workgroup a token, so that
 // its angles are formed once; from 512 workgroups on a token's heads are no
 // longer split, which would form them again.
