@@ -540,8 +540,9 @@ def _stream_on(device, stream):
 def _on_one_gpu(device, names, tensors):
     """Every tensor (None is skipped) lives on `device`, a GPU."""
     if device.type == "cuda":
+        index = device.index
         for t in tensors:
-            if t is not None and t.device != device:
+            if t is not None and t.get_device() != index:   # -1 for a host tensor
                 break
         else:
             return
@@ -1065,7 +1066,6 @@ def sgemv_rotary(q, q_out, positions, inv_freq, *, k=None, k_out=None, v=None, c
     sections = (pairs,) if sections is None else tuple(sections)
     if len(sections) != axes or axes > SGEMV_MAX_AXES or sum(sections) != pairs or min(sections) < 0:
         raise ValueError(f"sections: {sections}, expected {axes} numbers that sum to {pairs} (up to {SGEMV_MAX_AXES})")
-    _fits_int32("sgemv_rotary", tokens=tokens)
     device = first.device
     _on_one_gpu(device, ("q", "q_out", "k", "k_out", "v", "positions", "inv_freq", "slots", "cache"),
                 (q, q_out, k, k_out, v, positions, inv_freq, slots, None if cache is None else cache.k))
@@ -1109,12 +1109,15 @@ def sgemv_attn_paged(q, cache: KVCache, table, lengths, out, workspace, *, scale
             raise ValueError(f"lse: expected float32 [{batch}][{heads}], contiguous")
         zp = lse.data_ptr()
     wp, size = _space(workspace)
-    _fits_int32("sgemv_attn_paged", batch=batch, heads=heads, max_pages=columns, window=window)
+    try:
+        args = _ATTN.pack(qp, op, zp, tp, lp, wp, size, q_row, q_head, out_row, out_head, ld, code, batch, heads, columns,
+                          window, dim ** -0.5 if scale is None else scale, softcap, 0)
+    except struct.error:
+        _fits_int32("sgemv_attn_paged", batch=batch, heads=heads, max_pages=columns, window=window)
+        raise
     device = q.device
     _on_one_gpu(device, ("q", "cache", "table", "lengths", "out", "workspace", "lse"),
                 (q, cache.k, table, lengths, out, workspace, lse))
-    args = _ATTN.pack(qp, op, zp, tp, lp, wp, size, q_row, q_head, out_row, out_head, ld, code, batch, heads, columns,
-                      window, dim ** -0.5 if scale is None else scale, softcap, 0)
     _call(lib().sgemv_attn_paged, device, (args, cache.args, _stream_on(device, stream)), "sgemv_attn_paged")
 
 
@@ -1148,11 +1151,14 @@ def sgemv_beam_select(logits, scores, tokens, parents, scores_out, workspace, *,
             raise ValueError(f"finished: expected uint8 or bool [{batch}][{beams}], contiguous")
         fp = finished.data_ptr()
     wp, size = _space(workspace)
-    _fits_int32("sgemv_beam_select", batch=batch, beams=beams, vocab=vocab, choices=choices, end_token=end_token)
     device = logits.device
-    args = _BEAM.pack(lp, scores.data_ptr(), fp, _ints(tokens, "tokens", batch, choices),
-                      _ints(parents, "parents", batch, choices), scores_out.data_ptr(), wp, size, ld_batch, ld_beam, code,
-                      batch, beams, vocab, choices, end_token)
+    tp, pp = _ints(tokens, "tokens", batch, choices), _ints(parents, "parents", batch, choices)
+    try:
+        args = _BEAM.pack(lp, scores.data_ptr(), fp, tp, pp, scores_out.data_ptr(), wp, size, ld_batch, ld_beam, code,
+                          batch, beams, vocab, choices, end_token)
+    except struct.error:
+        _fits_int32("sgemv_beam_select", batch=batch, beams=beams, vocab=vocab, choices=choices, end_token=end_token)
+        raise
     _on_one_gpu(device, ("logits", "scores", "tokens", "parents", "scores_out", "workspace", "finished"),
                 (logits, scores, tokens, parents, scores_out, workspace, finished))
     _call(lib().sgemv_beam_select, device, (args, _stream_on(device, stream)), "sgemv_beam_select")
@@ -1193,14 +1199,17 @@ def _pages_call(name, table, lengths, refs, table_out, lengths_out, refs_out, wo
           _ints(count, "count", 1), _ints(status, "status", 2) if fork else 0]
     wp, size = _space(workspace)
     max_grow = 0 if slots is None else slots.shape[1]
-    _fits_int32(name, rows=rows, max_pages=columns, pages=pages, page_size=page_size, max_grow=max_grow)
     caches, packed = _caches(caches)
+    try:
+        args = _PAGES.pack(*at, wp, size, ld, ld_out, rows, columns, pages, page_size, max_grow, len(caches))
+    except struct.error:
+        _fits_int32(name, rows=rows, max_pages=columns, pages=pages, page_size=page_size, max_grow=max_grow)
+        raise
     device = table.device
     _on_one_gpu(device, ("table", "lengths", "refs", "table_out", "lengths_out", "refs_out", "parents", "grow", "slots",
                          "pairs", "count", "status", "workspace") + ("caches",) * len(caches),
                 (table, lengths, refs, table_out, lengths_out, refs_out, parents, grow, slots, pairs, count, status,
                  workspace) + tuple(c.k for c in caches))
-    args = _PAGES.pack(*at, wp, size, ld, ld_out, rows, columns, pages, page_size, max_grow, len(caches))
     _call(getattr(lib(), name), device, (args, packed, _stream_on(device, stream)), name)
 
 

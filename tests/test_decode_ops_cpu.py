@@ -201,6 +201,7 @@ def test_beam_refusals():
     refused(beam(parents=z(3, 7, dtype=torch.int32)), "parents: shape")
     refused(beam(scores_out=z(24)), "scores_out")
     refused(beam(finished=z(3, 4)), "finished")
+    refused(beam(end_token=1 << 31), "end_token")
     refused(beam(workspace=z(3)), "workspace")
 
 
@@ -227,6 +228,7 @@ def test_pages_refusals():
     refused(fork(pairs=i(4, 2)), "pairs: shape")
     refused(fork(status=None), "status")
     refused(fork(caches=[torch.zeros(3)]), "KVCache")
+    refused(fork(page_size=1 << 40), "page_size")
     refused(lambda: sgemv.sgemv_pages_copy([cache()], i(3)), "pairs")
     refused(lambda: sgemv.sgemv_pages_copy([], i(3, 3)), "at least one")
     refused(lambda: sgemv.sgemv_pages_copy([cache()], i(3, 3)), "must be a GPU tensor")
