@@ -65,7 +65,7 @@ constexpr int kParty = 16;                // pieces that are joined to one where
 constexpr int kMaxHeads = 2048;           // heads (of all sequences) of one launch
 constexpr int kCounterStep = 32;          // words between heads' arrival counters: one, and one for each party
 constexpr int kGrid = 512;                // workgroups that the GPU holds at once, two on a compute unit
-constexpr size_t kCounterBytes = (size_t)kMaxHeads * kCounterStep * 4;
+static_assert((size_t)kMaxHeads * kCounterStep * 4 <= kSgemvCounterBytes, "counters");
 constexpr uint32_t kCacheSC1 = 16;        // cache policy: coherent at device scope
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -813,7 +813,7 @@ extern "C" size_t sgemv_attn_workspace_bytes(int32_t batch, int32_t heads, int32
         dim > SGEMV_MAX_DIM || dim % 8)
         return 0;
     const int64_t groups = (int64_t)heads_kv * ((heads / heads_kv + kRows - 1) / kRows);
-    return kCounterBytes + (size_t)2 * (groups > kGrid ? groups : kGrid) * slot_bytes(dim);
+    return kSgemvCounterBytes + (size_t)2 * (groups > kGrid ? groups : kGrid) * slot_bytes(dim);
 }
 
 extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cache, void* stream) {
@@ -870,7 +870,7 @@ extern "C" int sgemv_attn_paged(const sgemv_attn_args* args, const sgemv_kv* cac
     a.k_page = kv.k_page * es; a.k_token = kv.k_token * es; a.k_head = kv.k_head * es;
     a.v_page = kv.v_page * es; a.v_token = kv.v_token * es; a.v_head = kv.v_head * es;
     a.counters = static_cast<uint32_t*>(p.workspace);
-    a.partial = static_cast<uint8_t*>(p.workspace) + kCounterBytes;
+    a.partial = static_cast<uint8_t*>(p.workspace) + kSgemvCounterBytes;
     a.q_row = p.q_row; a.q_head = p.q_head; a.out_row = p.out_row; a.out_head = p.out_head; a.ld_table = p.ld_table;
     a.page = sgemv_div(kv.page_size);
     a.pages = kv.pages;

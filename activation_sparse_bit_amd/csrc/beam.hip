@@ -43,7 +43,7 @@ constexpr int kMostTied = 6 * kThreads; // a part's values to be ranked, before 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kFar = 67108864.0f;    // 2^26: as far from zero a float may be off from v L by 2, and ever more beyond
 constexpr int kCounterStep = 16;       // words between arrival counters
-constexpr size_t kCounterBytes = (size_t)kMaxBatch * kCounterStep * 4;
+static_assert((size_t)kMaxBatch * kCounterStep * 4 <= kSgemvCounterBytes, "counters");
 
 struct Args {
     const uint8_t* logits;
@@ -658,7 +658,7 @@ extern "C" size_t sgemv_beam_workspace_bytes(int32_t batch, int32_t beams, int32
     int64_t records = entries * beams * parts_of(vocab, 4);
     const int64_t finer = 512 < entries * beams * parts_of(vocab, 1) ? 512 : entries * beams * parts_of(vocab, 1);
     if (finer > records) records = finer;
-    return kCounterBytes + (size_t)records * (choices + 1) * 8;
+    return kSgemvCounterBytes + (size_t)records * (choices + 1) * 8;
 }
 
 extern "C" int sgemv_beam_select(const sgemv_beam_args* args, void* stream) {
@@ -690,7 +690,7 @@ extern "C" int sgemv_beam_select(const sgemv_beam_args* args, void* stream) {
     }
     Args a;
     a.counters = static_cast<uint32_t*>(p.workspace);
-    a.parts_out = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes);
+    a.parts_out = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(p.workspace) + kSgemvCounterBytes);
     a.ld_batch = p.ld_batch;
     a.ld_beam = p.ld_beam;
     a.beams = p.beams;

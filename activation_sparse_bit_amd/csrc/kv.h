@@ -4,6 +4,10 @@
 
 #include "internal.h"
 
+// What every workspace of these calls begins with: arrival counters, zero
+// between calls, whichever call it is, so that one workspace serves them all.
+constexpr size_t kSgemvCounterBytes = (size_t)1 << 18;
+
 inline bool sgemv_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 inline int sgemv_size_of(int type) { return type == SGEMV_F32 ? 4 : type == SGEMV_E4M3 ? 1 : 2; }

@@ -695,7 +695,7 @@ extern "C" size_t sgemv_pages_workspace_bytes(int32_t rows, int32_t max_pages, i
     if (!sizes_ok(rows, max_pages, pages)) return 0;
     const size_t fork = up((size_t)rows * max_pages * 4) + up((size_t)pages * 4) + up((size_t)pages * 8) + up((size_t)rows * 16);
     const size_t compact = up(((size_t)pages / kBlock + 2) * 4) + 3 * up((size_t)pages * 4);
-    return 256 + (fork > compact ? fork : compact);
+    return kSgemvCounterBytes + (fork > compact ? fork : compact);
 }
 
 extern "C" int sgemv_pages_fork(const sgemv_pages_args* args, const sgemv_kv* caches, void* stream) {
@@ -710,7 +710,7 @@ extern "C" int sgemv_pages_fork(const sgemv_pages_args* args, const sgemv_kv* ca
         w += up(n);
         return at;
     };
-    a.counter = reinterpret_cast<uint32_t*>(take(256));
+    a.counter = reinterpret_cast<uint32_t*>(take(kSgemvCounterBytes));
     a.staged = reinterpret_cast<int32_t*>(take((size_t)p.rows * p.max_pages * 4));
     a.free_list = reinterpret_cast<int32_t*>(take((size_t)p.pages * 4));
     a.mark = reinterpret_cast<int32_t*>(take((size_t)p.pages * 8));
@@ -755,7 +755,7 @@ extern "C" int sgemv_pages_compact(const sgemv_pages_args* args, const sgemv_kv*
         return at;
     };
     a.blocks = (p.pages + kBlock - 1) / kBlock;
-    a.counter = reinterpret_cast<uint32_t*>(take(256));
+    a.counter = reinterpret_cast<uint32_t*>(take(kSgemvCounterBytes));
     a.before = reinterpret_cast<int32_t*>(take(((size_t)p.pages / kBlock + 2) * 4));
     a.target = reinterpret_cast<int32_t*>(take((size_t)p.pages * 4));
     a.source = reinterpret_cast<int32_t*>(take((size_t)p.pages * 4));

@@ -604,8 +604,8 @@ int sgemv_block_norm(const sgemv_norm* a, void* stream);
  * device, results are bitwise reproducible, and every call may be captured
  * into a graph.  Calls with a workspace take one that is zero-filled once by
  * the caller; they leave its counters at zero again, so it serves any number
- * of later calls of any shape it is large enough for, one after the other:
- * calls that share a workspace (graphs that were captured with the same one
+ * of later ones of these calls, of any shape that it is large enough for, one
+ * after the other: calls that share a workspace (graphs that were captured with the same one
  * among them) must not run at the same time.
  * ------------------------------------------------------------------------ */
 

@@ -210,3 +210,21 @@ def test_two_searches_at_once():
     torch.cuda.synchronize()
     for d, ref in zip((a, b), want):
         assert all(torch.equal(x, y) for x, y in zip(d.state(), ref))
+
+
+def test_one_workspace_for_all():
+    """The calls of a step take turns in one workspace, which each leaves fit for the next."""
+    d = Decoder("f16")
+    want = []
+    for _ in range(STEPS):
+        d.step()
+        want.append(d.state())
+    d.reset()
+    d.ws_pages = d.ws_attn = d.ws_beam = max((d.ws_pages, d.ws_attn, d.ws_beam), key=lambda t: t.numel())
+    moved, count = torch.zeros(len(d.refs), 3, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    scratch = d.table.clone(), d.refs.clone()
+    for n, ref in enumerate(want):
+        d.step()
+        assert all(torch.equal(a, b) for a, b in zip(d.state(), ref)), n
+        d.s.sgemv_pages_compact(d.table, d.lengths, d.refs, *scratch, d.ws_pages, page_size=PAGE, pairs=moved, count=count)
+    assert int(d.ws_attn[:1 << 18].count_nonzero()) == 0
