@@ -10,6 +10,10 @@
 // eight tokens, and those eight tokens are just what its slots of the second
 // product's operand want, so probabilities never leave their lane, and the
 // running maximum, its correction and the output belong to the lane's head.
+// A probability is given to the second product as the sum of two numbers of the
+// inputs' type (16 bits of it in bf16, 22 in fp16): twice its matrix instructions,
+// which the stream hides (48 x 24000 tokens 676 us with one, 673 with two; one
+// sequence of 640 tokens 9.3 and 9.6), and an output that is rounded once.
 // Values are read in rows (16 bytes a lane, whole rows by neighbouring lanes);
 // a lane that reads eight tokens' eight elements turns them by byte permutes
 // into eight operands of eight tokens each.  Keys are read in whole lines of 128
@@ -115,8 +119,8 @@ __device__ __forceinline__ float head_sum(float v) {
 struct F16 {
     using pair = half2_t;
     using frag = half8_t;
-    // Probabilities are held 2^15 times their size: fp16 then keeps those down to 2^-29 of the largest exactly as
-    // well as it keeps the largest.
+    // Probabilities are held 2^15 times their size: of two numbers of fp16 the first then keeps those down to 2^-29 of the
+    // largest as well as it keeps the largest, and the second is never off by more than 2^-40 of it.
     static constexpr float kLift = 15.0f;
     static __device__ __forceinline__ float4_t mfma(frag a, frag b, float4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -124,6 +128,8 @@ struct F16 {
     static __device__ __forceinline__ uint32_t two(float a, float b) {
         return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
     }
+    static __device__ __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(half2_t, w)[0]; }
+    static __device__ __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(half2_t, w)[1]; }
     static __device__ __forceinline__ uint16_t one(float a) { return __builtin_bit_cast(uint16_t, (_Float16)a); }
     template <bool HIGH>
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
@@ -141,6 +147,8 @@ struct BF16 {
     static __device__ __forceinline__ uint32_t two(float a, float b) {
         return __builtin_bit_cast(uint32_t, bf2_t{(__bf16)a, (__bf16)b});
     }
+    static __device__ __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+    static __device__ __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
     static __device__ __forceinline__ uint16_t one(float a) { return __builtin_bit_cast(uint16_t, (__bf16)a); }
     template <bool HIGH>
     static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
@@ -367,7 +375,7 @@ struct Attention {
     }
 
     // One step with keys and values that were loaded: 32 tokens from t0 on, some of them in [lo, len).
-    __device__ __forceinline__ void step(const Args& a, Tile& tile, const Span& span, int t0, float z_scale) {
+    __device__ __forceinline__ void step(const Args& a, Tile& tile, const Span& span, int t0, float z_scale, bool halves) {
         const int lane = threadIdx.x & 63, g = lane >> 4;
         uint4_t (&kr)[2][KLOADS] = tile.kr;
         uint32_t (&vr)[8][VB][VWORDS] = tile.vr;
@@ -442,8 +450,16 @@ struct Attention {
             sum += t[j];
         }
         l += sum;
-        const uint4_t pw = {T::two(t[0], t[1]), T::two(t[2], t[3]), T::two(t[4], t[5]), T::two(t[6], t[7])};
-        const auto pf = __builtin_bit_cast(typename T::frag, pw);
+        // A probability meets the values as the sum of two numbers of the type, the second what the first leaves off: 16 bits
+        // of it (bf16) or 22 (fp16).  One alone, 8 or 11 bits, was off by up to half a step of the output more.  The second
+        // may be zero or below, which an infinite value would make NaN: such tokens are taken with two equal halves.
+        uint4_t pw, rw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            pw[i] = halves ? T::two(0.5f * t[2 * i], 0.5f * t[2 * i + 1]) : T::two(t[2 * i], t[2 * i + 1]);
+            rw[i] = halves ? pw[i] : T::two(t[2 * i] - T::low(pw[i]), t[2 * i + 1] - T::high(pw[i]));
+        }
+        const auto pf = __builtin_bit_cast(typename T::frag, pw), rf = __builtin_bit_cast(typename T::frag, rw);
 #pragma unroll
         for (int nb = 0; nb < VB; ++nb)
 #pragma unroll
@@ -464,8 +480,11 @@ struct Attention {
                     lo[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
                     hi[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
                 }
-                o[nb][2 * r2] = T::mfma(__builtin_bit_cast(typename T::frag, lo), pf, o[nb][2 * r2]);
-                o[nb][2 * r2 + 1] = T::mfma(__builtin_bit_cast(typename T::frag, hi), pf, o[nb][2 * r2 + 1]);
+                const auto v0 = __builtin_bit_cast(typename T::frag, lo), v1 = __builtin_bit_cast(typename T::frag, hi);
+                o[nb][2 * r2] = T::mfma(v0, rf, o[nb][2 * r2]);
+                o[nb][2 * r2 + 1] = T::mfma(v1, rf, o[nb][2 * r2 + 1]);
+                o[nb][2 * r2] = T::mfma(v0, pf, o[nb][2 * r2]);
+                o[nb][2 * r2 + 1] = T::mfma(v1, pf, o[nb][2 * r2 + 1]);
             }
 #pragma unroll
         for (int nb = 0; nb < VB; ++nb)
@@ -645,22 +664,32 @@ struct Attention {
             float z_scale = a.scale * kLog2e;
             if (a.softcap > 0.0f) z_scale = a.scale;
             if (E4M3 && a.k_scale) z_scale *= a.k_scale[kvh];
-            m = -INFINITY;
-            l = 0.0f;
-#pragma unroll
-            for (int nb = 0; nb < VB; ++nb)
-#pragma unroll
-                for (int r = 0; r < VW; ++r) o[nb][r] = float4_t{0, 0, 0, 0};
             bool bad = span.bad;
             const int32_t* pages = a.table + b * a.ld_table;
             // this wavefront's steps of the piece: tokens t0, t0 + kUnit, ... below `last`
             const int64_t k_off = kvh * a.k_head, v_off = kvh * a.v_head;
-            int t0 = span.first + c0 * kUnit + wave * kTile;
+            const int start = span.first + c0 * kUnit + wave * kTile;
             const int last = span.first + c1 * kUnit < span.len ? span.first + c1 * kUnit : span.len;
-            for (; t0 < last; t0 += kUnit) {
-                Tile tile;
-                load(a, tile, find(a, pages, t0, span.len), k_off, v_off, bad);
-                step(a, tile, span, t0, z_scale);
+            for (bool halves = false;; halves = true) {   // a second time only where the first made NaN
+                m = -INFINITY;
+                l = 0.0f;
+#pragma unroll
+                for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                    for (int r = 0; r < VW; ++r) o[nb][r] = float4_t{0, 0, 0, 0};
+                for (int t0 = start; t0 < last; t0 += kUnit) {
+                    Tile tile;
+                    load(a, tile, find(a, pages, t0, span.len), k_off, v_off, bad);
+                    step(a, tile, span, t0, z_scale, halves);
+                }
+                bool nan = false;
+#pragma unroll
+                for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                    for (int r = 0; r < VW; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) nan |= o[nb][r][i] != o[nb][r][i];
+                if (halves || !__ballot(nan)) break;
             }
             l = head_sum(l);
             if (bad) l = NAN;

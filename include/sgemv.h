@@ -728,8 +728,9 @@ typedef struct sgemv_attn_args {
  *   - What stands in a page outside of the seen tokens has no effect, NaN and
  *     infinities included.
  * Products of the cache's type (8-bit values as `type`) with fp32 sums;
- * softmax statistics in fp32; probabilities are rounded to `type` for the
- * product with the values; one rounding at the end.
+ * softmax statistics in fp32; probabilities meet the values as the sum of two
+ * numbers of `type` (16 bits of them in bf16, 22 in fp16; as one number where a
+ * sequence and key head have values that are not finite); one rounding at the end.
  *   kv->type  `type`, or SGEMV_E4M3
  *   out       refused where it overlaps an input
  * EINVAL for NULL, a bad type or value, differing heads or dim, an overlap;
