@@ -313,18 +313,22 @@ struct Attention {
         }
     }
 
-    // The pages of 32 tokens from t0 on, some of them below len.
-    static __device__ __forceinline__ Where find(const Args& a, const int32_t* pages, int t0, int len) {
+    // The pages of 32 tokens from t0 on, some of them in [lo, len).  Entries that no such token is in are not looked at, they
+    // may be those of pages that were given back: what is asked for beside is read from a seen token's page.
+    static __device__ __forceinline__ Where find(const Args& a, const int32_t* pages, int t0, const Span& span) {
         Where w;
         w.bad = false;
-        if constexpr (WHOLE) {
-            const int t1 = t0 + 16 < len ? t0 + 16 : t0, p0 = divide(t0, a.page), p1 = divide(t1, a.page);
-            w.id[0] = pages[p0];
-            w.id[1] = pages[p1];
-            w.in[0] = t0 - p0 * (int)a.page.d;
-            w.in[1] = t1 - p1 * (int)a.page.d;
+        if constexpr (WHOLE) {   // a page holds all 16 of a half or none
+            const int ta = t0 + 16 <= span.lo ? t0 + 16 : t0, tb = t0 + 16 < span.len ? t0 + 16 : t0;
+            const int pa = divide(ta, a.page), pb = divide(tb, a.page);
+            w.id[0] = pages[pa];
+            w.id[1] = pages[pb];
+            w.in[0] = ta - pa * (int)a.page.d;
+            w.in[1] = tb - pb * (int)a.page.d;
         } else {
-            const int lane = threadIdx.x & 31, t = t0 + lane < len ? t0 + lane : len - 1, p = divide(t, a.page);
+            int t = t0 + (int)(threadIdx.x & 31);
+            t = t < span.lo ? span.lo : t < span.len ? t : span.len - 1;
+            const int p = divide(t, a.page);
             w.id[0] = pages[p];
             w.in[0] = t - p * (int)a.page.d;
         }
@@ -679,7 +683,7 @@ struct Attention {
                     for (int r = 0; r < VW; ++r) o[nb][r] = float4_t{0, 0, 0, 0};
                 for (int t0 = start; t0 < last; t0 += kUnit) {
                     Tile tile;
-                    load(a, tile, find(a, pages, t0, span.len), k_off, v_off, bad);
+                    load(a, tile, find(a, pages, t0, span), k_off, v_off, bad);
                     step(a, tile, span, t0, z_scale, halves);
                 }
                 bool nan = false;

@@ -1087,7 +1087,8 @@ def sgemv_attn_paged(q, cache: KVCache, table, lengths, out, workspace, *, scale
     cache's; table is int32 [batch][max_pages], lengths int32 [batch], both on
     the device; workspace is uint8, zero-filled once, of
     sgemv_attn_workspace_bytes(batch, heads, kv heads, dim).  scale defaults
-    to 1 / sqrt(dim); window: only the last tokens are seen (0: all);
+    to 1 / sqrt(dim); window: only the last tokens are seen (0: all), and
+    table entries whose tokens all lie before it may be anything;
     softcap * tanh(z / softcap) of every score (0: none); lse (optional)
     float32 [batch][heads] receives the logarithm of the sum of exponentials."""
     code = _type_code(q, "q")

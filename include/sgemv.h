@@ -724,7 +724,8 @@ typedef struct sgemv_attn_args {
  *   - length 0: out is 0 and lse -infinity.
  *   - A length below 0 or beyond max_pages * page_size, or a table entry in use
  *     outside 0 .. pages - 1, makes that sequence's out and lse NaN; nothing out
- *     of range is read.
+ *     of range is read.  An entry is in use where a seen token is in its page:
+ *     pages that lie before the window may have been given back.
  *   - What stands in a page outside of the seen tokens has no effect, NaN and
  *     infinities included.
  * Products of the cache's type (8-bit values as `type`) with fp32 sums;
