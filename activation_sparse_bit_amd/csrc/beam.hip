@@ -217,6 +217,7 @@ __device__ __forceinline__ int threads_per(int count) {
 template <int PER, class V, class F>
 __device__ __forceinline__ int tighten(V* list, int count, int most, int n, uint32_t* bounds, uint32_t* left, F key) {
     if (count <= most) return count;   // most is at least n, so every wavefront's share has n/4 items
+    __syncthreads();                   // `count` may come from *left: every thread has read it before it is cleared
     const int tid = threadIdx.x;
     constexpr int kWaves = kThreads / 64;
     const int at = (tid & 63) * kWaves + tid / 64;   // neighbours, which are alike, over the wavefronts
