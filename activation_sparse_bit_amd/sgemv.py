@@ -1132,7 +1132,9 @@ def sgemv_beam_select(logits, scores, tokens, parents, scores_out, workspace, *,
     [batch][beams][vocab] (float16, bfloat16, float32, any strides with the
     last dimension contiguous), scores float32 [batch][beams]; tokens and
     parents int32 and scores_out float32 [batch][choices] receive the largest
-    score + log softmax(logits), largest first.  finished (optional) uint8
+    score + log softmax(logits), largest first; where there are fewer, token and
+    parent are -1.  sgemv_pages_fork takes rows, -1 for those: torch.where(parents < 0,
+    -1, parents + beams * arange(batch)[:, None]), and no growth.  finished (optional) uint8
     [batch][beams]: such a beam goes on with end_token at its own score.
     workspace is uint8, zero-filled once, of sgemv_beam_workspace_bytes(batch,
     beams, vocab, choices)."""

@@ -773,8 +773,11 @@ typedef struct sgemv_beam_args {
  * logits are all none, or one of whose logits is +infinity, has none.  Where
  * there are fewer than `choices`, the rest are token -1, parent -1, score
  * -infinity.  s is formed and compared in 64 bits, from fp32 exponentials, and
- * rounded to fp32 at the end.  `parents` is what sgemv_pages_fork takes (as row
- * batch * beams + parent).
+ * rounded to fp32 at the end.  What sgemv_pages_fork takes, where a search's
+ * beams are rows b * beams .. b * beams + beams - 1, is
+ *   parent < 0 ? -1 : b * beams + parent
+ * (row b * beams - 1 is another search's), with a growth of 0 for such a row: it
+ * ends, and its score of -infinity keeps it out of later choices.
  * EINVAL for NULL, a bad type or end_token, an overlap; ESIZE for sizes,
  * strides, too small a workspace (sgemv_beam_workspace_bytes); EALIGN for
  * pointers.
