@@ -416,7 +416,7 @@ struct Attention {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float x = t[j] * (1.0f / a.softcap);
-                t[j] = a.softcap * kLog2e * tanhf(x);
+                t[j] = a.softcap * tanhf(x) * kLog2e;   // a cap's own product would be infinite above 2.36e38
             }
         }
         if (edge) {
