@@ -261,6 +261,23 @@ SgemvRows extent(const Operand& o, int64_t tokens, int dim, int size) {
     return SgemvRows{o.p, 1, 0, ((tokens - 1) * o.row + span) * size};
 }
 
+// Whether two operands share bytes.  Heads that lie between each other's (queries, keys and values side by side head by
+// head) are told apart by their places within the smallest stride, where both have the same strides, all multiples of it.
+bool share(const Operand& a, const Operand& b, int64_t tokens, int dim, int size) {
+    if (!a.p || !b.p) return false;
+    if (a.heads > 1 && b.heads > 1 && a.head == b.head && (tokens == 1 || a.row == b.row)) {
+        const int64_t step = tokens > 1 && a.row < a.head ? a.row : a.head;
+        if (a.head % step == 0 && (tokens == 1 || a.row % step == 0)) {
+            const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+            const int64_t bytes = step * size, width = (int64_t)dim * size;
+            const int64_t off = pb > pa ? (int64_t)((pb - pa) % (uintptr_t)bytes)
+                                        : (int64_t)(((uintptr_t)bytes - (pa - pb) % (uintptr_t)bytes) % (uintptr_t)bytes);
+            if (off >= width && off + width <= bytes) return false;
+        }
+    }
+    return sgemv_overlap(extent(a, tokens, dim, size), extent(b, tokens, dim, size));
+}
+
 }  // namespace
 
 extern "C" int sgemv_rotary(const sgemv_rotary_args* args, const sgemv_kv* cache, void* stream) {
@@ -322,15 +339,19 @@ extern "C" int sgemv_rotary(const sgemv_rotary_args* args, const sgemv_kv* cache
     const auto replaces = [&](const Operand& out, const Operand& in) {   // the very same elements
         return out.p == in.p && (p.tokens == 1 || out.row == in.row) && (in.heads == 1 || out.head == in.head);
     };
+    const Operand* const turned[2] = {&q_out, &k_out};
+    const Operand* const read[3] = {&q, &k, &v};
     for (int i = 0; i < 4; ++i) {
-        for (const SgemvRows& in : ins) {
-            if (i == 0 && in.p == p.q && &in == &ins[0] && replaces(q_out, q)) continue;
-            if (i == 1 && &in == &ins[1] && replaces(k_out, k)) continue;
-            if (sgemv_overlap(outs[i], in)) return SGEMV_EINVAL;
+        for (int j = 0; j < 8; ++j) {
+            if (i == 0 && j == 0 && replaces(q_out, q)) continue;
+            if (i == 1 && j == 1 && replaces(k_out, k)) continue;
+            if (i < 2 && j < 3 ? share(*turned[i], *read[j], p.tokens, p.dim, size) : sgemv_overlap(outs[i], ins[j]))
+                return SGEMV_EINVAL;
         }
         // keys and values may be parts of one buffer: the caller's strides keep them apart
         for (int j = i + 1; j < 4; ++j)
-            if (!(i == 2 && j == 3) && sgemv_overlap(outs[i], outs[j])) return SGEMV_EINVAL;
+            if (i == 0 && j == 1 ? share(q_out, k_out, p.tokens, p.dim, size) : i < 2 && sgemv_overlap(outs[i], outs[j]))
+                return SGEMV_EINVAL;
     }
 
     Args a = {};

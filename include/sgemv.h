@@ -684,8 +684,10 @@ typedef struct sgemv_rotary_args {
  *   rounded to nearest even and held at +-448; NaN stays NaN.
  * Two tokens with one slot leave either one's values there.
  * q_out and k_out may be q and k themselves (same address and strides); any
- * other overlap of an output with another operand is refused.  Operands need
- * the alignment of their elements (16-byte addresses and strides are faster).
+ * other overlap of an output with another operand is refused.  Operands of the
+ * same strides may lie between each other, token by token or head by head;
+ * others are taken as the range from their first value to their last.  They
+ * need the alignment of their elements (16-byte addresses and strides are faster).
  * EINVAL for NULL, a bad type, flag or section, an overlap; ESIZE for sizes and
  * strides (positions: ld_positions >= tokens); EALIGN for pointers, and for a
  * cache's strides; EINVAL too where kv and the arguments differ in heads or dim.
