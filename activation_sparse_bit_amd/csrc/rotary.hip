@@ -5,9 +5,11 @@
 //
 // A workgroup takes one token (and, for few tokens, a part of its heads): it
 // forms the token's cosines and sines once, in LDS, and turns every head with
-// them.  Angles are reduced in 64 bits, where a position of 2^31 turns still
-// leaves 2^-24 of a turn; cosine and sine follow in fp32 from the part of a
-// turn that is left.
+// them.  Angles are reduced in 64 bits, which three roundings leave off by at most
+// 2^-51 of the number of turns: a position up to 2^31 with an inv_freq up to 1 is
+// under 2^28.4 turns, and off by less than 2^-22 of one; with larger ones, by
+// more in proportion.  Cosine and sine follow in fp32 from the part of a turn that
+// is left.
 //
 // Nothing is computed on the way that a stream of q, k and v does not hide:
 // bound by HBM for a prompt (16384 tokens, 64 query and 8 key heads of 128, three

@@ -912,7 +912,9 @@ class KVCache:
     strides with the last dimension contiguous (a [pages][heads][page_size][dim]
     buffer is passed as buffer.transpose(1, 2), keys and values of one buffer as
     its slices).  k_scale and v_scale, float32 [heads], say what a stored 1 of
-    an 8-bit cache stands for (None: 1)."""
+    an 8-bit cache stands for (None: 1).  Addresses, shape and strides are those
+    of the tensors when the KVCache is made: one whose storage is replaced later
+    (resize_, set_, .data) needs a new KVCache."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if not _TYPES:

@@ -676,8 +676,9 @@ typedef struct sgemv_rotary_args {
  * SGEMV_ROTARY_ADJACENT; elements from 2 * pairs on pass as they are.  axis(i)
  * is 0 for the first sections[0] pairs, 1 for the next sections[1], and so on;
  * with SGEMV_ROTARY_STRIPED pairs go to axes 0, 1, ... in turn, leaving out
- * axes that have all of theirs.  Angles are taken in 64 bits (positions are
- * exact up to 2^31), cosine, sine and the turn in 32, each result rounded once.
+ * axes that have all of theirs.  Angles are taken in 64 bits (off by at most
+ * 2^-51 of themselves: 2^-22 of a turn for positions up to 2^31 where inv_freq is
+ * at most 1), cosine, sine and the turn in 32, each result rounded once.
  *   q -> q_out; k -> k_out (optional) and, with a cache `kv`, to its slot;
  *   v -> its slot as it is.  A slot below 0 or beyond the cache writes
  *   nothing.  With SGEMV_E4M3 the cache holds value / scale of the head,
@@ -844,6 +845,8 @@ typedef struct sgemv_pages_args {
  *   caches  host array of `layers` caches of one geometry (pages, page_size,
  *           heads, dim, type, strides), pages and page_size as here; may be
  *           NULL with layers 0.  More layers: sgemv_pages_copy over the pairs.
+ *           No two of a layer's or of different layers' places may share bytes
+ *           (interleaved in one buffer is fine): that is not checked.
  * EINVAL for NULL, overlaps, caches that differ; ESIZE for sizes, strides, too
  * small a workspace; EALIGN for pointers.
  */
@@ -864,7 +867,7 @@ int sgemv_pages_compact(const sgemv_pages_args* a, const sgemv_kv* caches, void*
  * max_pairs) rows of pairs (device [max_pairs][3]; count NULL: all).  Rows with
  * an id outside the cache, or no tokens, are left out; more tokens than
  * page_size count as page_size.  A page that is the target of one pair should
- * be neither source nor target of another.
+ * be neither source nor target of another; caches as for sgemv_pages_fork.
  */
 int sgemv_pages_copy(const sgemv_kv* caches, int32_t layers, const int32_t* pairs,
                      const int32_t* count, int32_t max_pairs, void* stream);
