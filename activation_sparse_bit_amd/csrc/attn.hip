@@ -19,10 +19,10 @@
 // into eight operands of eight tokens each.  Keys are read in whole lines of 128
 // bytes too, eight tokens a load, and two loads exchange half their lanes (eight
 // apart) to become the operands of 16 tokens.  Loads of whole lines can be
-// marked as used once (48 x 24000 tokens, 64 heads on 8: 752 us, 664 marked,
-// which is 6.5 TB/s); where a row is no whole number of lines, or several
-// workgroups read it, that costs more than it gives (heads of 96: 108 us
-// against 95; 20 heads a key head: 150 against 137).
+// marked as used once (48 x 24000 tokens in bf16, 64 heads of 128 on 8: 742 us,
+// 675 marked); where a row is no whole number of lines, or several workgroups
+// read it, that costs more than it gives (16 x 8192 tokens, 64 heads of 96 on 8: 97
+// us, 116 marked; 160 heads of 128 on 8: 135 and 157).
 //
 // Work is split evenly whatever the lengths: the units of 128 tokens of all
 // sequences form one line that is cut into equal runs, and a workgroup takes
@@ -31,14 +31,14 @@
 // one time.  A run's first and last piece may be part of a sequence; such
 // pieces go to the workspace, and the last workgroup of that sequence and head
 // to arrive joins them in the order of the tokens (above 2 * 16 pieces, each 16
-// of them first: one key head over 131000 tokens 30 us, in one step 86).  The
+// of them first: one key head over 131000 tokens 27 us, in one step 86).  The
 // cut follows from the lengths alone, so results do not depend on timing.
 //
-// Bound by HBM: 48 x 24000 tokens, 64 heads of 128 on 8, 4.7 GB in 664-678 us,
-// 6.4-6.5 TB/s; 16 sequences of up to 32768 tokens 60 us, 4.5 TB/s, since some
+// Bound by HBM: 48 x 20011..24000 tokens, 64 heads of 128 on 8, 4.32 GB in 673-676
+// us, 6.4 TB/s; 16 sequences of up to 32768 tokens 61 us, 4.4 TB/s, since some
 // 15 us go to the first loads, the last steps of uneven workgroups and the
 // join.  Loads alone, without the products, take the same times.  A short
-// sequence (640 tokens, 9.3 us) waits for a launch, two dependent reads (table,
+// sequence (640 tokens, 9.5 us) waits for a launch, two dependent reads (table,
 // keys), one hand-off and a join.
 #include <hip/hip_runtime.h>
 

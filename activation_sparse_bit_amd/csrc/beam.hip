@@ -21,7 +21,7 @@
 // Bound by latency: one request with 4 beams of 32003 takes 10.9 us, of which
 // 5 go to the last workgroup's choice (three dependent reads past the caches and
 // some ten barriers).  48 x 8 beams of 100003 in bf16, 63 MB without
-// those that have ended, take 34.6 us, vector units half busy: loads and sums alone take 19, the parts' choices 7, the last
+// those that have ended, take 34 us, vector units half busy: loads and sums alone take 19, the parts' choices 7, the last
 // entries' 8; smaller parts (2048 or 4096 values each) take 44, since each
 // part's choice costs much the same whatever its size.
 #include <hip/hip_runtime.h>
