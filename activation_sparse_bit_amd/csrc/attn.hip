@@ -379,7 +379,7 @@ struct Attention {
     }
 
     // One step with keys and values that were loaded: 32 tokens from t0 on, some of them in [lo, len).
-    __device__ __forceinline__ void step(const Args& a, Tile& tile, const Span& span, int t0, float z_scale, bool halves) {
+    __device__ __forceinline__ void step(const Args& a, Tile& tile, const Span& span, int t0, float z_scale, bool twice) {
         const int lane = threadIdx.x & 63, g = lane >> 4;
         uint4_t (&kr)[2][KLOADS] = tile.kr;
         uint32_t (&vr)[8][VB][VWORDS] = tile.vr;
@@ -456,12 +456,12 @@ struct Attention {
         l += sum;
         // A probability meets the values as the sum of two numbers of the type, the second what the first leaves off: 16 bits
         // of it (bf16) or 22 (fp16).  One alone, 8 or 11 bits, was off by up to half a step of the output more.  The second
-        // may be zero or below, which an infinite value would make NaN: such tokens are taken with two equal halves.
+        // may be zero or below, which an infinite value would make NaN: there the first is taken twice, and the sums halved.
         uint4_t pw, rw;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            pw[i] = halves ? T::two(0.5f * t[2 * i], 0.5f * t[2 * i + 1]) : T::two(t[2 * i], t[2 * i + 1]);
-            rw[i] = halves ? pw[i] : T::two(t[2 * i] - T::low(pw[i]), t[2 * i + 1] - T::high(pw[i]));
+            pw[i] = T::two(t[2 * i], t[2 * i + 1]);
+            rw[i] = twice ? pw[i] : T::two(t[2 * i] - T::low(pw[i]), t[2 * i + 1] - T::high(pw[i]));
         }
         const auto pf = __builtin_bit_cast(typename T::frag, pw), rf = __builtin_bit_cast(typename T::frag, rw);
 #pragma unroll
@@ -674,7 +674,7 @@ struct Attention {
             const int64_t k_off = kvh * a.k_head, v_off = kvh * a.v_head;
             const int start = span.first + c0 * kUnit + wave * kTile;
             const int last = span.first + c1 * kUnit < span.len ? span.first + c1 * kUnit : span.len;
-            for (bool halves = false;; halves = true) {   // a second time only where the first made NaN
+            for (bool twice = false;; twice = true) {   // once more only where the first time made NaN
                 m = -INFINITY;
                 l = 0.0f;
 #pragma unroll
@@ -684,7 +684,7 @@ struct Attention {
                 for (int t0 = start; t0 < last; t0 += kUnit) {
                     Tile tile;
                     load(a, tile, find(a, pages, t0, span), k_off, v_off, bad);
-                    step(a, tile, span, t0, z_scale, halves);
+                    step(a, tile, span, t0, z_scale, twice);
                 }
                 bool nan = false;
 #pragma unroll
@@ -693,7 +693,14 @@ struct Attention {
                     for (int r = 0; r < VW; ++r)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) nan |= o[nb][r][i] != o[nb][r][i];
-                if (halves || !__ballot(nan)) break;
+                if (twice) {
+#pragma unroll
+                    for (int nb = 0; nb < VB; ++nb)
+#pragma unroll
+                        for (int r = 0; r < VW; ++r) o[nb][r] *= 0.5f;
+                    break;
+                }
+                if (!__ballot(nan)) break;
             }
             l = head_sum(l);
             if (bad) l = NAN;

@@ -132,3 +132,22 @@ def test_infinite_values_stay_infinite(x):
     assert (np.abs(rest[0] - rest[1]) <= 1.01 * u + 2 * u * np.abs(rest[1])).all()
     p.v[pages[70], 5, 1, 7] = float("-inf")   # both signs: NaN, as in the formula
     assert np.isnan(f64(p.run(scale=1.0)[0])[0, 4:, 7]).all()
+
+
+def test_an_infinite_value_of_the_least_probability():
+    """fp16's smallest probability is 2^-40 of the largest, and rounded from a little above half of that: an infinite value
+    there is no NaN, one of a probability below is (0 times it), as with finite arithmetic of that type."""
+    p = levels(30, [40], 64, 16, "f16", Hkv=1, G=4)
+    put_values(p, torch.ones(p.v.shape))
+    pages = p.table[0].tolist()
+    k = torch.zeros(p.k.shape)
+    k[..., 0] = -8.0                                  # all others vanish
+    k[pages[0], 0, 0, 0] = 0.0
+    k[pages[1], 1, 0, 0] = -1.0
+    p.k.copy_(k.half().to(base.DEV))
+    log2 = np.log(2.0)
+    p.dev[0].zero_()
+    p.dev[0][0, :, 0] = torch.tensor([39.2 * log2, 38.9 * log2, 30 * log2, log2]).half().to(base.DEV)
+    p.v[pages[1], 1, 0, 3] = float("inf")
+    out = f64(p.run(scale=1.0)[0])[0]
+    assert (out[:, 3] == np.inf).all() and (np.delete(out, 3, axis=1) == 1).all(), out[:, 2:5]
